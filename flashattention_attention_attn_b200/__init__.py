@@ -14,6 +14,12 @@ library built from ``csrc/`` (C ABI declared in ``include/attn.h``):
                              and lse, and
   attn_lse_merge             the merge of such partials (context-parallel
                              decode, see dist_util.context_parallel_decode)
+  paged_cache_plan           block-table entries, cache slots and positions of a
+                             step's new tokens, from the requests' lengths
+  rope_axes_fwd, _bwd        rotary positions with several axes, and the gradient
+  rope_axes_paged_append     the same with k and v written into the paged cache
+                             (_fp8: as e4m3 codes)
+  paged_attn_prefill_fp8     paged_attn_prefill over an e4m3 cache (also _checked)
 
 The Python functions here only marshal arguments into that library; there is
 no CPU fallback.  Importing the package does not load the library; the first
@@ -26,8 +32,11 @@ _BINDING_NAMES = {
     "attn_fwd", "attn_fwd_varlen", "paged_attn_decode", "paged_attn_decode_fp8", "paged_attn_decode_noalloc",
     "paged_attn_prefill", "paged_attn_decode_checked", "paged_attn_decode_fp8_checked", "paged_attn_prefill_checked",
     "paged_attn_decode_partial", "attn_lse_merge",
+    "paged_cache_plan", "rope_axis_map", "rope_axes_fwd", "rope_axes_bwd", "rope_axes_paged_append",
+    "rope_axes_paged_append_fp8", "paged_attn_prefill_fp8", "paged_attn_prefill_fp8_checked",
     "attn_check_support", "attn_status_string", "attn_read_device_status", "attn_selftest_bounded_wait", "library",
     "library_path", "AttnError", "ATTN_DEVSTATUS_TIMEOUT", "ATTN_DEVSTATUS_BAD_BLOCK", "ATTN_DEVSTATUS_BAD_SEQLEN",
+    "ATTN_DEVSTATUS_NO_BLOCK",
 }
 
 

@@ -19,6 +19,7 @@ ATTN_OK = 0
 ATTN_DEVSTATUS_TIMEOUT = 0x1
 ATTN_DEVSTATUS_BAD_BLOCK = 0x2
 ATTN_DEVSTATUS_BAD_SEQLEN = 0x4
+ATTN_DEVSTATUS_NO_BLOCK = 0x8
 _lib = None
 
 
@@ -68,6 +69,23 @@ def library() -> ctypes.CDLL:
         lib.paged_attn_decode_partial.restype = c_int
         lib.attn_lse_merge.argtypes = [vp, vp, c_int, c_int, c_int, c_int, vp, vp]
         lib.attn_lse_merge.restype = c_int
+        i64, c_bytes = ctypes.c_int64, ctypes.c_char_p
+        lib.paged_cache_plan.argtypes = [vp] * 4 + [c_int] * 5 + [vp] * 7
+        lib.paged_cache_plan.restype = c_int
+        rope_head = [vp, vp, vp, vp, c_bytes]
+        lib.rope_axes_fwd.argtypes = rope_head + [c_int] * 6 + [i64] * 3 + [c_int, vp, vp, i64, i64, vp]
+        lib.rope_axes_fwd.restype = c_int
+        lib.rope_axes_bwd.argtypes = lib.rope_axes_fwd.argtypes
+        lib.rope_axes_bwd.restype = c_int
+        append_head = [vp] * 5 + [c_bytes, vp] + [c_int] * 6 + [i64] * 4 + [c_int] * 3
+        lib.rope_axes_paged_append.argtypes = append_head + [vp] * 4
+        lib.rope_axes_paged_append.restype = c_int
+        lib.rope_axes_paged_append_fp8.argtypes = append_head + [c_float] * 2 + [vp] * 4
+        lib.rope_axes_paged_append_fp8.restype = c_int
+        lib.paged_attn_prefill_fp8.argtypes = [vp] * 6 + [c_int] * 9 + [c_float] * 3 + [c_int] + [vp] * 3
+        lib.paged_attn_prefill_fp8.restype = c_int
+        lib.paged_attn_prefill_fp8_checked.argtypes = [vp] * 6 + [c_int] * 10 + [c_float] * 3 + [c_int] + [vp] * 3
+        lib.paged_attn_prefill_fp8_checked.restype = c_int
         lib.attn_check_support.argtypes = [c_int]
         lib.attn_check_support.restype = c_int
         lib.attn_status_string.argtypes = [c_int]
@@ -219,6 +237,129 @@ def paged_attn_decode_noalloc(q, k_cache, v_cache, block_table, seq_lens, B, Hq,
                                              int(max_blocks), int(num_splits), _ptr(o), _stream(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "paged_attn_decode_noalloc")
+
+
+def paged_cache_plan(cached_lens, new_lens, free_blocks, pos_offsets, B, num_free, block_size, max_blocks, max_tokens,
+                     block_table, seq_lens, cu_seqlens_q, slot_map, positions, blocks_taken, stream=None) -> None:
+    """Block-table entries, slots, positions and prefix sums of a step's new
+    tokens from the requests' lengths (see attn.h)."""
+    rc = library().paged_cache_plan(_ptr(cached_lens), _ptr(new_lens), _ptr(free_blocks), _ptr(pos_offsets), int(B),
+                                    int(num_free), int(block_size), int(max_blocks), int(max_tokens),
+                                    _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens_q), _ptr(slot_map),
+                                    _ptr(positions), _ptr(blocks_taken), _stream(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "paged_cache_plan")
+
+
+def rope_axis_map(sections, interleaved=False) -> bytes:
+    """freq_axis of the rotary calls: sections[a] pairs rotate with axis a.
+
+    In contiguous runs (the first sections[0] pairs with axis 0, and so on),
+    or, interleaved, dealt out in turn (axis 0, 1, .., 0, 1, ..) until a
+    section is used up.
+    """
+    left = [int(n) for n in sections]
+    if any(n < 0 for n in left) or len(left) > 255:
+        raise ValueError("sections: up to 255 counts of pairs, none negative")
+    if not interleaved:
+        return b"".join(bytes([a]) * n for a, n in enumerate(left))
+    out = bytearray()
+    while any(left):
+        for a, n in enumerate(left):
+            if n:
+                out.append(a)
+                left[a] = n - 1
+    return bytes(out)
+
+
+def _axis_bytes(freq_axis, rot_dim) -> bytes | None:
+    if freq_axis is None:
+        return None
+    axes = bytes(freq_axis)
+    if len(axes) != int(rot_dim) // 2:
+        raise ValueError(f"freq_axis has {len(axes)} entries, rot_dim {rot_dim} needs {int(rot_dim) // 2}")
+    return axes
+
+
+def rope_axes_fwd(q, k, positions, inv_freq, freq_axis, n_tokens, Hq, Hkv, d, rot_dim, num_axes, pos_stride, q_stride,
+                  k_stride, adjacent, q_out, k_out, q_out_stride, k_out_stride, stream=None) -> None:
+    """Rotary positions with several axes (see attn.h).  freq_axis: bytes or
+    ints, the axis of each of the rot_dim / 2 pairs (rope_axis_map), or None."""
+    rc = library().rope_axes_fwd(_ptr(q), _ptr(k), _ptr(positions), _ptr(inv_freq), _axis_bytes(freq_axis, rot_dim),
+                                 int(n_tokens), int(Hq), int(Hkv), int(d), int(rot_dim), int(num_axes),
+                                 int(pos_stride), int(q_stride), int(k_stride), int(bool(adjacent)), _ptr(q_out),
+                                 _ptr(k_out), int(q_out_stride), int(k_out_stride), _stream(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "rope_axes_fwd")
+
+
+def rope_axes_bwd(dq_out, dk_out, positions, inv_freq, freq_axis, n_tokens, Hq, Hkv, d, rot_dim, num_axes, pos_stride,
+                  dq_out_stride, dk_out_stride, adjacent, dq, dk, dq_stride, dk_stride, stream=None) -> None:
+    """Gradient of rope_axes_fwd (see attn.h)."""
+    rc = library().rope_axes_bwd(_ptr(dq_out), _ptr(dk_out), _ptr(positions), _ptr(inv_freq),
+                                 _axis_bytes(freq_axis, rot_dim), int(n_tokens), int(Hq), int(Hkv), int(d),
+                                 int(rot_dim), int(num_axes), int(pos_stride), int(dq_out_stride),
+                                 int(dk_out_stride), int(bool(adjacent)), _ptr(dq), _ptr(dk), int(dq_stride),
+                                 int(dk_stride), _stream(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "rope_axes_bwd")
+
+
+def rope_axes_paged_append(q, k, v, positions, inv_freq, freq_axis, slot_map, n_tokens, Hq, Hkv, d, rot_dim, num_axes,
+                           pos_stride, q_stride, k_stride, v_stride, adjacent, block_size, num_blocks, q_out, k_cache,
+                           v_cache, stream=None) -> None:
+    """rope_axes_fwd of q and k, with k and v written into the paged bf16
+    cache at slot_map (see attn.h)."""
+    rc = library().rope_axes_paged_append(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(inv_freq),
+                                          _axis_bytes(freq_axis, rot_dim), _ptr(slot_map), int(n_tokens), int(Hq),
+                                          int(Hkv), int(d), int(rot_dim), int(num_axes), int(pos_stride),
+                                          int(q_stride), int(k_stride), int(v_stride), int(bool(adjacent)),
+                                          int(block_size), int(num_blocks), _ptr(q_out), _ptr(k_cache),
+                                          _ptr(v_cache), _stream(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "rope_axes_paged_append")
+
+
+def rope_axes_paged_append_fp8(q, k, v, positions, inv_freq, freq_axis, slot_map, n_tokens, Hq, Hkv, d, rot_dim,
+                               num_axes, pos_stride, q_stride, k_stride, v_stride, adjacent, block_size, num_blocks,
+                               k_scale, v_scale, q_out, k_cache, v_cache, stream=None) -> None:
+    """rope_axes_paged_append into an FP8 e4m3 cache with per-tensor scales (see attn.h)."""
+    rc = library().rope_axes_paged_append_fp8(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(inv_freq),
+                                              _axis_bytes(freq_axis, rot_dim), _ptr(slot_map), int(n_tokens),
+                                              int(Hq), int(Hkv), int(d), int(rot_dim), int(num_axes),
+                                              int(pos_stride), int(q_stride), int(k_stride), int(v_stride),
+                                              int(bool(adjacent)), int(block_size), int(num_blocks), float(k_scale),
+                                              float(v_scale), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
+                                              _stream(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "rope_axes_paged_append_fp8")
+
+
+def paged_attn_prefill_fp8(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, B, Hq, Hkv, d, block_size,
+                           max_blocks, max_seqlen_q, total_q, causal, scale, k_scale, v_scale, num_splits, o, lse,
+                           stream=None) -> None:
+    """Chunked prefill against an FP8 e4m3 paged cache with per-tensor scales (see attn.h)."""
+    rc = library().paged_attn_prefill_fp8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
+                                          _ptr(cu_seqlens_q), int(B), int(Hq), int(Hkv), int(d), int(block_size),
+                                          int(max_blocks), int(max_seqlen_q), int(total_q), int(bool(causal)),
+                                          float(scale), float(k_scale), float(v_scale), int(num_splits), _ptr(o),
+                                          _ptr(lse), _stream(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "paged_attn_prefill_fp8")
+
+
+def paged_attn_prefill_fp8_checked(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, B, Hq, Hkv, d, block_size,
+                                   max_blocks, num_blocks, max_seqlen_q, total_q, causal, scale, k_scale, v_scale,
+                                   num_splits, o, lse, stream=None) -> None:
+    """paged_attn_prefill_fp8 for a pool of num_blocks blocks (see attn.h)."""
+    rc = library().paged_attn_prefill_fp8_checked(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+                                                  _ptr(seq_lens), _ptr(cu_seqlens_q), int(B), int(Hq), int(Hkv),
+                                                  int(d), int(block_size), int(max_blocks), int(num_blocks),
+                                                  int(max_seqlen_q), int(total_q), int(bool(causal)), float(scale),
+                                                  float(k_scale), float(v_scale), int(num_splits), _ptr(o), _ptr(lse),
+                                                  _stream(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "paged_attn_prefill_fp8_checked")
 
 
 def attn_check_support(device: int = 0) -> int:

@@ -23,7 +23,8 @@ LIB_DIR = os.path.join(PKG_DIR, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libattn_b200.so")
 
 SOURCES = ["attn_api.cu"]
-HEADERS = ["sm100_ptx.cuh", "prefill_sm100.cuh", "decode_paged.cuh", "decode_paged_fp8.cuh"]
+HEADERS = ["sm100_ptx.cuh", "prefill_sm100.cuh", "decode_paged.cuh", "decode_paged_fp8.cuh", "paged_plan.cuh",
+           "rope_axes.cuh", "prefill_fp8_sm100.cuh"]
 
 
 def nvcc_path() -> str:

@@ -14,7 +14,10 @@
 #include "attn.h"
 #include "decode_paged.cuh"
 #include "decode_paged_fp8.cuh"
+#include "paged_plan.cuh"
+#include "prefill_fp8_sm100.cuh"
 #include "prefill_sm100.cuh"
+#include "rope_axes.cuh"
 #include "sm100_ptx.cuh"
 
 namespace attn {
@@ -35,6 +38,7 @@ struct DeviceState {
   int status = ATTN_ERR_CUDA;  // result of the support check
   int sms = 0;
   bool attrs_set = false;
+  bool prefill8_ok = false;  // the FP8 chunk kernel's register split fits its launch
   cudaMemPool_t pool = nullptr;
 };
 
@@ -132,6 +136,7 @@ int prepare_device(int dev, DeviceState* st) {
       {reinterpret_cast<const void*>(decode::paged_decode_split<64>), decode::smem_bytes<64>()},
       {reinterpret_cast<const void*>(decode::paged_decode_split<128>), decode::smem_bytes<128>()},
       {reinterpret_cast<const void*>(decode::paged_decode_split_fp8), decode::smem_bytes_fp8()},
+      {reinterpret_cast<const void*>(prefill8::prefill_fp8_sm100), prefill8::smem_bytes()},
   };
   for (const auto& k : kernels)
     if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.bytes)) !=
@@ -139,6 +144,13 @@ int prepare_device(int dev, DeviceState* st) {
       cudaGetLastError();
       return ATTN_ERR_CUDA;
     }
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, prefill8::prefill_fp8_sm100) != cudaSuccess) {
+    cudaGetLastError();
+    return ATTN_ERR_CUDA;
+  }
+  st->prefill8_ok = static_cast<long long>(fa.numRegs) * prefill8::kThreads >=
+                    256LL * prefill8::kSoftmaxRegs + 128LL * prefill8::kOtherRegs;
   cudaMemPoolProps props;
   std::memset(&props, 0, sizeof(props));
   props.allocType = cudaMemAllocationTypePinned;
@@ -987,4 +999,357 @@ extern "C" int paged_attn_decode_noalloc(const void* q, const void* k_cache, con
                                      num_splits, o, stream, st->sms, scratch);
   return launch_decode_noalloc<128>(q, k_cache, v_cache, block_table, seq_lens, B, Hq, Hkv, max_blocks,
                                     num_splits, o, stream, st->sms, scratch);
+}
+
+// ---------------------------------------------------------------------------
+// The serving step around the paged cache: plan, rotary positions with the
+// cache write, attention of the new tokens over the FP8 cache.
+// ---------------------------------------------------------------------------
+namespace attn {
+namespace {
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// 3-D bf16 map over the packed queries [total_q, Hq, 128]: one box is the
+// `tokens` x G heads x 64 columns of a query tile.
+int make_map_q_tile(CUtensorMap* map, const void* base, int total_q, int Hq, int G, int tokens) {
+  constexpr int D = prefill8::kD;
+  cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(Hq), cuuint64_t(total_q)};
+  cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(Hq) * D * 2};
+  cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(tokens)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+                              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+// 2-D byte map over an e4m3 pool seen as [tokens, Hkv * 128]: box (128, 16),
+// one head of one block.
+int make_map_pool_e4m3(CUtensorMap* map, const void* base, int Hkv, int num_blocks, CUtensorMapSwizzle swizzle) {
+  constexpr int D = prefill8::kD;
+  cuuint64_t dims[2] = {cuuint64_t(Hkv) * D, cuuint64_t(num_blocks) * decode::kBlock};
+  cuuint64_t strides[1] = {cuuint64_t(Hkv) * D};
+  cuuint32_t box[2] = {D, 16};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
+}
+
+int launch_prefill_fp8(const void* q, const void* kc, const void* vc, const int32_t* table, const int32_t* lens,
+                       const int32_t* cu_q, void* o, float* lse, int B, int max_q, int total_q, int Hq, int Hkv,
+                       int max_blocks, int num_blocks, int causal, float scale, float k_scale, float v_scale,
+                       int num_splits, cudaStream_t stream, const DeviceState* st) {
+  constexpr int D = prefill8::kD;
+  const int G = Hq / Hkv;
+  prefill8::Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.tok_tile = prefill8::kBM / G;
+  CUtensorMap mq, mk, mv;
+  if (make_map_q_tile(&mq, q, total_q, Hq, G, p.tok_tile) ||
+      make_map_pool_e4m3(&mk, kc, Hkv, num_blocks, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      make_map_pool_e4m3(&mv, vc, Hkv, num_blocks, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return ATTN_ERR_CUDA;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.cu_q = cu_q;
+  p.block_table = table;
+  p.seq_lens = lens;
+  p.max_blocks = max_blocks;
+  p.num_blocks = num_blocks;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = G;
+  p.g_magic = (65536 + G - 1) / G;
+  p.total_q = total_q;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = scale * k_scale * 1.4426950408889634f;
+  p.v_scale = v_scale;
+  const int rows_cta = 2 * p.tok_tile;
+  if (max_q > total_q) max_q = total_q;
+  p.num_mblocks = (max_q + rows_cta - 1) / rows_cta;
+  long long items = static_cast<long long>(p.num_mblocks) * B;
+  if (B <= 32) {
+    const long long bound = (static_cast<long long>(total_q) + static_cast<long long>(B) * (rows_cta - 1)) / rows_cta;
+    if (bound < items) items = bound;
+    p.items = static_cast<int>(items);
+  }
+  const int max_tiles = (max_blocks + 7) / 8;
+  long long chunk;
+  if (num_splits <= 0) {
+    const long long waves = B == 1 ? 1 : 3;
+    chunk = (items * Hkv * max_tiles + waves * st->sms - 1) / (waves * st->sms);
+    if (chunk < 4) chunk = 4;
+  } else {
+    chunk = (max_tiles + num_splits - 1) / num_splits;
+  }
+  if (chunk > max_tiles) chunk = max_tiles;
+  p.chunk = static_cast<int>(chunk);
+  p.splits = (max_tiles + p.chunk - 1) / p.chunk;
+  const long long grid = items * Hkv * p.splits;
+  const long long merge_grid =
+      (static_cast<long long>(total_q) * Hq + prefill8::kCombineWarps - 1) / prefill8::kCombineWarps;
+  if (grid > 0x7fffffffLL || merge_grid > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+
+  void* ws = nullptr;
+  if (p.splits > 1) {
+    const size_t rows = static_cast<size_t>(p.splits) * total_q * Hq;
+    const size_t bytes = rows * (D + 1) * sizeof(float);
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
+      cudaGetLastError();
+      return ATTN_ERR_CUDA;
+    }
+    const cudaError_t ae = (cap == cudaStreamCaptureStatusActive)
+                               ? cudaMallocAsync(&ws, bytes, stream)
+                               : cudaMallocFromPoolAsync(&ws, bytes, st->pool, stream);
+    if (ae != cudaSuccess) {
+      cudaGetLastError();
+      return ATTN_ERR_CUDA;
+    }
+    p.part_o = static_cast<float*>(ws);
+    p.part_lse = p.part_o + rows * D;
+  }
+  int rc = launch_pdl(prefill8::prefill_fp8_sm100, dim3(static_cast<unsigned>(grid)), dim3(prefill8::kThreads),
+                      prefill8::smem_bytes(), stream, mq, mk, mv, p);
+  if (rc == ATTN_OK && p.splits > 1)
+    rc = launch_pdl(prefill8::prefill_fp8_combine, dim3(static_cast<unsigned>(merge_grid)),
+                    dim3(prefill8::kCombineWarps * 32), 0, stream, static_cast<const float*>(p.part_o),
+                    static_cast<const float*>(p.part_lse), cu_q, p.o, lse, B, Hq, total_q, p.splits);
+  if (ws != nullptr) cudaFreeAsync(ws, stream);
+  return rc;
+}
+
+int prefill_fp8_entry(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_table,
+                      const int32_t* seq_lens, const int32_t* cu_seqlens_q, int B, int Hq, int Hkv, int d,
+                      int block_size, int max_blocks, int num_blocks, int max_seqlen_q, int total_q, int causal,
+                      float scale, float k_scale, float v_scale, int num_splits, void* o, float* lse,
+                      cudaStream_t stream) {
+  if (max_seqlen_q < 0 || total_q < 0) return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale) || !(k_scale > 0.f) || !std::isfinite(k_scale) || !(v_scale > 0.f) ||
+      !std::isfinite(v_scale))
+    return ATTN_ERR_INVALID_ARG;
+  int rc = check_paged_common(B, Hq, Hkv, d, block_size, max_blocks, num_blocks);
+  if (rc != ATTN_OK) return rc;
+  if (B == 0 || total_q == 0 || max_seqlen_q == 0) return ATTN_OK;
+  if (q == nullptr || k_cache == nullptr || v_cache == nullptr || block_table == nullptr || seq_lens == nullptr ||
+      cu_seqlens_q == nullptr || o == nullptr)
+    return ATTN_ERR_INVALID_ARG;
+  if (d != prefill8::kD || Hq / Hkv > prefill8::kBM) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned4(lse) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(cu_seqlens_q))
+    return ATTN_ERR_UNSUPPORTED;
+  DeviceState* st = nullptr;
+  rc = current_device_state(&st);
+  if (rc != ATTN_OK) return rc;
+  if (!st->prefill8_ok) return ATTN_ERR_UNSUPPORTED;
+  return launch_prefill_fp8(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, o, lse, B, max_seqlen_q, total_q,
+                            Hq, Hkv, max_blocks, num_blocks, causal, scale, k_scale, v_scale, num_splits, stream, st);
+}
+
+// Host checks and launch shared by the rotary entry points (mode: rope::k*).
+int rope_entry(int mode, rope::Params& p, const uint8_t* freq_axis, int rot_dim, int num_axes, cudaStream_t stream) {
+  if (p.n < 0 || p.Hq < 0 || p.Hkv < 0 || p.d <= 0 || rot_dim < 0 || num_axes <= 0) return ATTN_ERR_INVALID_ARG;
+  if (rot_dim > p.d || (mode != rope::kPlain && p.Hkv == 0)) return ATTN_ERR_INVALID_ARG;
+  if (mode == rope::kCacheFp8 && (!(p.k_scale > 0.f) || !std::isfinite(p.k_scale) || !(p.v_scale > 0.f) ||
+                                  !std::isfinite(p.v_scale)))
+    return ATTN_ERR_INVALID_ARG;
+  if (p.n == 0 || (p.Hq == 0 && p.Hkv == 0)) return ATTN_OK;
+  if ((p.Hq > 0 && (p.q == nullptr || p.q_out == nullptr)) || (p.Hkv > 0 && p.k == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (p.positions == nullptr || p.inv_freq == nullptr)) return ATTN_ERR_INVALID_ARG;
+  if (mode == rope::kPlain ? (p.Hkv > 0 && p.k_out == nullptr)
+                           : (p.v == nullptr || p.slot_map == nullptr || p.k_cache == nullptr || p.v_cache == nullptr ||
+                              p.num_blocks <= 0))
+    return ATTN_ERR_INVALID_ARG;
+  if (p.d != 128 && (p.d != 64 || mode == rope::kCacheFp8)) return ATTN_ERR_UNSUPPORTED;
+  if (rot_dim % 16 != 0 || num_axes > 255 || p.num_blocks > kMaxPoolBlocks) return ATTN_ERR_UNSUPPORTED;
+  if (p.pos_stride < 0) return ATTN_ERR_INVALID_ARG;
+  p.half = rot_dim / 2;
+  for (int i = 0; i < p.half; ++i) {
+    p.axis[i] = freq_axis != nullptr ? freq_axis[i] : 0;
+    if (p.axis[i] >= num_axes) return ATTN_ERR_INVALID_ARG;
+  }
+  const long long wq = static_cast<long long>(p.Hq) * p.d, wk = static_cast<long long>(p.Hkv) * p.d;
+  const bool has_k_out = mode == rope::kPlain;
+  if (p.q_stride < wq || p.q_out_stride < wq || p.k_stride < wk || (has_k_out ? p.k_out_stride < wk : p.v_stride < wk))
+    return ATTN_ERR_INVALID_ARG;  // rows would overlap
+  if ((p.q_stride | p.k_stride | p.v_stride | p.q_out_stride | p.k_out_stride) & 7) return ATTN_ERR_UNSUPPORTED;
+  if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.v) || !aligned16(p.q_out) || !aligned16(p.k_out) ||
+      !aligned16(p.k_cache) || !aligned16(p.v_cache))
+    return ATTN_ERR_UNSUPPORTED;
+  if (!aligned4(p.positions) || !aligned4(p.inv_freq) || !aligned4(p.slot_map)) return ATTN_ERR_UNSUPPORTED;
+  if (static_cast<long long>(p.Hq + 2LL * p.Hkv) * (p.d / 16) * rope::kMaxTokens > 0x7fffffffLL)
+    return ATTN_ERR_UNSUPPORTED;
+  DeviceState* st = nullptr;
+  int rc = current_device_state(&st);
+  if (rc != ATTN_OK) return rc;
+  p.tpc = 1;
+  while (p.tpc * 2 <= rope::kThreads / (p.half > 0 ? p.half : rope::kMaxHalf) && p.tpc * 2 <= rope::kMaxTokens &&
+         p.n / (p.tpc * 2) >= 4 * st->sms)
+    p.tpc *= 2;
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.n) + p.tpc - 1) / p.tpc));
+  const dim3 block(rope::kThreads);
+  if (mode == rope::kPlain) return launch_pdl(rope::rope_axes_kernel<rope::kPlain>, grid, block, 0, stream, p);
+  if (mode == rope::kCacheBf16) return launch_pdl(rope::rope_axes_kernel<rope::kCacheBf16>, grid, block, 0, stream, p);
+  return launch_pdl(rope::rope_axes_kernel<rope::kCacheFp8>, grid, block, 0, stream, p);
+}
+
+rope::Params rope_params(const void* q, const void* k, const int32_t* positions, const float* inv_freq, int n, int Hq,
+                         int Hkv, int d, int64_t pos_stride, int64_t q_stride, int64_t k_stride, int adjacent,
+                         void* q_out, int64_t q_out_stride) {
+  rope::Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.n = n;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.d = d;
+  p.pos_stride = pos_stride;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.adjacent = adjacent ? 1 : 0;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.q_out_stride = q_out_stride;
+  p.sign = 1.f;
+  p.k_scale = p.v_scale = 1.f;
+  return p;
+}
+
+int rope_append_entry(int mode, const void* q, const void* k, const void* v, const int32_t* positions,
+                      const float* inv_freq, const uint8_t* freq_axis, const int32_t* slot_map, int n, int Hq, int Hkv,
+                      int d, int rot_dim, int num_axes, int64_t pos_stride, int64_t q_stride, int64_t k_stride,
+                      int64_t v_stride, int adjacent, int block_size, int num_blocks, float k_scale, float v_scale,
+                      void* q_out, void* k_cache, void* v_cache, cudaStream_t stream) {
+  if (block_size <= 0) return ATTN_ERR_INVALID_ARG;
+  if (block_size != rope::kBlock) return ATTN_ERR_UNSUPPORTED;
+  rope::Params p = rope_params(q, k, positions, inv_freq, n, Hq, Hkv, d, pos_stride, q_stride, k_stride, adjacent, q_out,
+                               static_cast<int64_t>(Hq) * d);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.v_stride = v_stride;
+  p.slot_map = slot_map;
+  p.num_blocks = num_blocks;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  return rope_entry(mode, p, freq_axis, rot_dim, num_axes, stream);
+}
+
+}  // namespace
+}  // namespace attn
+
+extern "C" int paged_cache_plan(const int32_t* cached_lens, const int32_t* new_lens, const int32_t* free_blocks,
+                                const int32_t* pos_offsets, int B, int num_free, int block_size, int max_blocks,
+                                int max_tokens, int32_t* block_table, int32_t* seq_lens, int32_t* cu_seqlens_q,
+                                int32_t* slot_map, int32_t* positions, int32_t* blocks_taken, attn_stream_t stream) {
+  if (B < 0 || num_free < 0 || block_size <= 0 || max_tokens < 0) return ATTN_ERR_INVALID_ARG;
+  if (B > 0 && max_blocks <= 0) return ATTN_ERR_INVALID_ARG;
+  if (block_size != plan::kBlock || max_blocks > kMaxPoolBlocks) return ATTN_ERR_UNSUPPORTED;
+  if (cu_seqlens_q == nullptr || blocks_taken == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (B > 0 && (cached_lens == nullptr || new_lens == nullptr || block_table == nullptr || seq_lens == nullptr))
+    return ATTN_ERR_INVALID_ARG;
+  if ((num_free > 0 && free_blocks == nullptr) || (max_tokens > 0 && (slot_map == nullptr || positions == nullptr)))
+    return ATTN_ERR_INVALID_ARG;
+  const void* ptrs[] = {cached_lens, new_lens, free_blocks, pos_offsets, block_table, seq_lens,
+                        cu_seqlens_q, slot_map, positions, blocks_taken};
+  for (const void* x : ptrs)
+    if (!aligned4(x)) return ATTN_ERR_UNSUPPORTED;
+  DeviceState* st = nullptr;
+  int rc = current_device_state(&st);
+  if (rc != ATTN_OK) return rc;
+  plan::Params p;
+  p.cached = cached_lens;
+  p.fresh = new_lens;
+  p.free_blocks = free_blocks;
+  p.pos_offsets = pos_offsets;
+  p.table = block_table;
+  p.seq_lens = seq_lens;
+  p.cu = cu_seqlens_q;
+  p.slot_map = slot_map;
+  p.positions = positions;
+  p.blocks_taken = blocks_taken;
+  p.B = B;
+  p.num_free = num_free;
+  p.max_blocks = max_blocks;
+  p.max_tokens = max_tokens;
+  // a token per thread, at most one CTA per SM
+  int grid = (max_tokens + plan::kThreads - 1) / plan::kThreads;
+  if (max_tokens > 0x7fffffff - plan::kThreads) grid = st->sms;
+  if (grid > st->sms) grid = st->sms;
+  if (grid < 1) grid = 1;
+  return launch_pdl(plan::paged_cache_plan_kernel, dim3(grid), dim3(plan::kThreads), 0,
+                    reinterpret_cast<cudaStream_t>(stream), p);
+}
+
+extern "C" int rope_axes_fwd(const void* q, const void* k, const int32_t* positions, const float* inv_freq,
+                             const uint8_t* freq_axis, int n_tokens, int Hq, int Hkv, int d, int rot_dim, int num_axes,
+                             int64_t pos_stride, int64_t q_stride, int64_t k_stride, int adjacent, void* q_out,
+                             void* k_out, int64_t q_out_stride, int64_t k_out_stride, attn_stream_t stream) {
+  rope::Params p = rope_params(q, k, positions, inv_freq, n_tokens, Hq, Hkv, d, pos_stride, q_stride, k_stride, adjacent,
+                               q_out, q_out_stride);
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.k_out_stride = k_out_stride;
+  return rope_entry(rope::kPlain, p, freq_axis, rot_dim, num_axes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int rope_axes_bwd(const void* dq_out, const void* dk_out, const int32_t* positions, const float* inv_freq,
+                             const uint8_t* freq_axis, int n_tokens, int Hq, int Hkv, int d, int rot_dim, int num_axes,
+                             int64_t pos_stride, int64_t dq_out_stride, int64_t dk_out_stride, int adjacent, void* dq,
+                             void* dk, int64_t dq_stride, int64_t dk_stride, attn_stream_t stream) {
+  rope::Params p = rope_params(dq_out, dk_out, positions, inv_freq, n_tokens, Hq, Hkv, d, pos_stride, dq_out_stride,
+                               dk_out_stride, adjacent, dq, dq_stride);
+  p.k_out = static_cast<__nv_bfloat16*>(dk);
+  p.k_out_stride = dk_stride;
+  p.sign = -1.f;
+  return rope_entry(rope::kPlain, p, freq_axis, rot_dim, num_axes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int rope_axes_paged_append(const void* q, const void* k, const void* v, const int32_t* positions,
+                                      const float* inv_freq, const uint8_t* freq_axis, const int32_t* slot_map,
+                                      int n_tokens, int Hq, int Hkv, int d, int rot_dim, int num_axes,
+                                      int64_t pos_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                      int adjacent, int block_size, int num_blocks, void* q_out, void* k_cache,
+                                      void* v_cache, attn_stream_t stream) {
+  return rope_append_entry(rope::kCacheBf16, q, k, v, positions, inv_freq, freq_axis, slot_map, n_tokens, Hq, Hkv, d,
+                           rot_dim, num_axes, pos_stride, q_stride, k_stride, v_stride, adjacent, block_size,
+                           num_blocks, 1.f, 1.f, q_out, k_cache, v_cache, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int rope_axes_paged_append_fp8(const void* q, const void* k, const void* v, const int32_t* positions,
+                                          const float* inv_freq, const uint8_t* freq_axis, const int32_t* slot_map,
+                                          int n_tokens, int Hq, int Hkv, int d, int rot_dim, int num_axes,
+                                          int64_t pos_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                          int adjacent, int block_size, int num_blocks, float k_scale, float v_scale,
+                                          void* q_out, void* k_cache, void* v_cache, attn_stream_t stream) {
+  return rope_append_entry(rope::kCacheFp8, q, k, v, positions, inv_freq, freq_axis, slot_map, n_tokens, Hq, Hkv, d,
+                           rot_dim, num_axes, pos_stride, q_stride, k_stride, v_stride, adjacent, block_size,
+                           num_blocks, k_scale, v_scale, q_out, k_cache, v_cache,
+                           reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int paged_attn_prefill_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                      const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_seqlens_q,
+                                      int B, int Hq, int Hkv, int d, int block_size, int max_blocks, int max_seqlen_q,
+                                      int total_q, int causal, float scale, float k_scale, float v_scale,
+                                      int num_splits, void* o, float* lse, attn_stream_t stream) {
+  return prefill_fp8_entry(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, B, Hq, Hkv, d, block_size,
+                           max_blocks, kMaxPoolBlocks, max_seqlen_q, total_q, causal, scale, k_scale, v_scale,
+                           num_splits, o, lse, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int paged_attn_prefill_fp8_checked(const void* q, const void* k_cache, const void* v_cache,
+                                              const int32_t* block_table, const int32_t* seq_lens,
+                                              const int32_t* cu_seqlens_q, int B, int Hq, int Hkv, int d,
+                                              int block_size, int max_blocks, int num_blocks, int max_seqlen_q,
+                                              int total_q, int causal, float scale, float k_scale, float v_scale,
+                                              int num_splits, void* o, float* lse, attn_stream_t stream) {
+  return prefill_fp8_entry(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, B, Hq, Hkv, d, block_size,
+                           max_blocks, num_blocks, max_seqlen_q, total_q, causal, scale, k_scale, v_scale, num_splits,
+                           o, lse, reinterpret_cast<cudaStream_t>(stream));
 }

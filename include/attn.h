@@ -73,6 +73,9 @@ typedef enum {
 /* A paged call met a seq_lens entry below 0 or above max_blocks * block_size
  * (more positions than its table row names): it was clamped into that range. */
 #define ATTN_DEVSTATUS_BAD_SEQLEN 0x4
+/* paged_cache_plan needed more blocks than its free list holds: the table
+ * entries and slots that found none are -1. */
+#define ATTN_DEVSTATUS_NO_BLOCK 0x8
 
 /*
  * attn_fwd - dense prefill attention with grouped-query heads.
@@ -407,6 +410,187 @@ int paged_attn_decode_noalloc(const void* q, const void* k_cache, const void* v_
                               const int32_t* block_table, const int32_t* seq_lens,
                               int B, int Hq, int Hkv, int d, int block_size, int max_blocks,
                               int num_splits, void* o, attn_stream_t stream);
+
+/*
+ * The serving step around the paged cache.  The page "Snelle attention-kernels
+ * en operatorfusie versnellen AI-modellen", section "FlashAttention-type
+ * aandacht en gepagineerde aandacht", describes the cache these calls fill:
+ * fixed-size blocks and a block table that maps every logical position to a
+ * physical block.  A step is
+ *   paged_cache_plan              lengths -> table entries, slots, positions
+ *   rope_axes_paged_append[_fp8]  q, k, v -> rotated q, cache
+ *   paged_attn_prefill[_fp8] or paged_attn_decode[_fp8]
+ * on one stream, with nothing read back by the host.
+ */
+
+/*
+ * paged_cache_plan - block tables and slot maps from the requests' lengths.
+ *
+ *   cached_lens  [B] int32 tokens of sequence b in the cache (c_b)
+ *   new_lens     [B] int32 tokens that this step adds (n_b, 0 allowed)
+ *   free_blocks  [num_free] int32 ids of free blocks, taken from the front
+ *   pos_offsets  [B] int32 added to the positions of sequence b, or NULL
+ *   block_table  [B, max_blocks] int32 (updated): its first ceil(c_b / 16)
+ *                entries are the sequence's blocks; entries up to
+ *                ceil((c_b + n_b) / 16) are written, the others left alone
+ *   seq_lens     [B] int32 (written): c_b + n_b
+ *   cu_seqlens_q [B + 1] int32 (written): prefix sums of n_b
+ *   slot_map     [max_tokens] int32 (written): for the token at position p of
+ *                its sequence, block id * 16 + p % 16; -1 behind the last
+ *                token (a batch padded for a captured graph) and for a token
+ *                without a place
+ *   positions    [max_tokens] int32 (written): p + pos_offsets[b]; 0 behind
+ *                the last token
+ *   blocks_taken [1] int32 (written): blocks that the new tokens need.  The
+ *                free list is not changed: the caller drops that many ids
+ *                from its front.
+ *
+ *   New blocks are handed out sequence by sequence, in order.  Outputs must
+ *   not overlap inputs (block_table is both).
+ *   Malformed lengths set ATTN_DEVSTATUS_BAD_SEQLEN: negative ones count as 0;
+ *   rows behind max_tokens are dropped (cu_seqlens_q ends at max_tokens); a
+ *   sequence keeps at most max_blocks * 16 tokens, and tokens past that get
+ *   slot -1.  A free list that is too short sets ATTN_DEVSTATUS_NO_BLOCK
+ *   (entries and slots of -1; blocks_taken is what would have been needed),
+ *   and a partly filled last block whose table entry is no block id, or an
+ *   id that is none on the free list, sets ATTN_DEVSTATUS_BAD_BLOCK (slots
+ *   of -1).
+ *   Supported: block_size == 16; max_blocks < 2^27; any B (B == 0 writes
+ *   cu_seqlens_q[0], blocks_taken and the padding); 4-byte aligned pointers;
+ *   sm_100 device.
+ *   Errors: ATTN_ERR_INVALID_ARG for negative sizes, max_blocks <= 0 when
+ *   B > 0 or a null pointer to something of non-zero size;
+ *   ATTN_ERR_UNSUPPORTED otherwise outside the supported set.  No workspace.
+ */
+int paged_cache_plan(const int32_t* cached_lens, const int32_t* new_lens, const int32_t* free_blocks,
+                     const int32_t* pos_offsets, int B, int num_free, int block_size, int max_blocks,
+                     int max_tokens, int32_t* block_table, int32_t* seq_lens, int32_t* cu_seqlens_q,
+                     int32_t* slot_map, int32_t* positions, int32_t* blocks_taken, attn_stream_t stream);
+
+/*
+ * rope_axes_fwd - rotary positions with several axes.
+ *
+ *   q, k         rows of Hq * d and Hkv * d bf16, q_stride and k_stride
+ *                elements apart (columns of a fused projection will do)
+ *   positions    [num_axes] rows of n_tokens int32, pos_stride elements apart
+ *                (0: every axis reads the same row): the token's place on each
+ *                axis (time, height, width; one axis for text)
+ *   inv_freq     [rot_dim / 2] fp32: angle per step of each pair
+ *   freq_axis    HOST array of rot_dim / 2 bytes: the axis of each pair, or
+ *                NULL for axis 0 throughout (copied during the call)
+ *   adjacent     0: element i of a head's first rot_dim is paired with
+ *                element i + rot_dim / 2; otherwise element 2 i with 2 i + 1
+ *   q_out, k_out (written) as q and k, q_out_stride and k_out_stride elements
+ *                apart; may be q and k themselves with the same strides
+ *
+ *   Pair i of a head, (a, b), becomes (a cos x - b sin x, b cos x + a sin x)
+ *   with x = positions[freq_axis[i], token] * inv_freq[i]; elements from
+ *   rot_dim on are copied.  The angle is formed in fp64 and reduced there,
+ *   cos, sin and the rotation are fp32, the result is rounded once to bf16.
+ *   Hq or Hkv may be 0 (its pointers may then be NULL).
+ *   Supported: d in {64, 128}; rot_dim % 16 == 0; strides that are multiples
+ *   of 8; 16-byte aligned q, k, outputs; sm_100.  n_tokens == 0 is a no-op.
+ *   Errors: ATTN_ERR_INVALID_ARG for null pointers, negative sizes,
+ *   num_axes <= 0, rot_dim > d, an axis >= num_axes or a stride smaller than
+ *   the row; ATTN_ERR_UNSUPPORTED otherwise outside the supported set.  No
+ *   workspace.
+ */
+int rope_axes_fwd(const void* q, const void* k, const int32_t* positions, const float* inv_freq,
+                  const uint8_t* freq_axis, int n_tokens, int Hq, int Hkv, int d, int rot_dim, int num_axes,
+                  int64_t pos_stride, int64_t q_stride, int64_t k_stride, int adjacent, void* q_out,
+                  void* k_out, int64_t q_out_stride, int64_t k_out_stride, attn_stream_t stream);
+
+/*
+ * rope_axes_bwd - gradient of rope_axes_fwd: dq and dk (written) from the
+ * gradients of its outputs.  The rotation is orthogonal, so the gradient is
+ * the rotation by the negative angle.  Arguments, layouts, rounding and
+ * errors as rope_axes_fwd; dq and dk may be dq_out and dk_out.
+ */
+int rope_axes_bwd(const void* dq_out, const void* dk_out, const int32_t* positions, const float* inv_freq,
+                  const uint8_t* freq_axis, int n_tokens, int Hq, int Hkv, int d, int rot_dim, int num_axes,
+                  int64_t pos_stride, int64_t dq_out_stride, int64_t dk_out_stride, int adjacent, void* dq,
+                  void* dk, int64_t dq_stride, int64_t dk_stride, attn_stream_t stream);
+
+/*
+ * rope_axes_paged_append - rope_axes_fwd of q and k with the rotated k and v
+ * written into the paged cache.
+ *
+ *   v            rows of Hkv * d bf16, v_stride elements apart
+ *   slot_map     [n_tokens] int32: token t goes to slot slot_map[t] % 16 of
+ *                block slot_map[t] / 16; a negative slot is not written (its
+ *                q is rotated all the same).  A slot past the pool is not
+ *                written either and sets ATTN_DEVSTATUS_BAD_BLOCK.  Two
+ *                tokens must not share a slot: its content is then a mix.
+ *   num_blocks   physical blocks of the pool
+ *   q_out        [n_tokens, Hq, d] bf16 (written)
+ *   k_cache, v_cache [num_blocks, 16, Hkv, d] bf16 (written at the slots only)
+ *
+ *   Other arguments as rope_axes_fwd.  q_out may be q when q_stride is
+ *   Hq * d.
+ *   Supported and errors: as rope_axes_fwd; ATTN_ERR_INVALID_ARG also for
+ *   Hkv == 0 or num_blocks <= 0; block_size == 16; num_blocks < 2^27.
+ */
+int rope_axes_paged_append(const void* q, const void* k, const void* v, const int32_t* positions,
+                           const float* inv_freq, const uint8_t* freq_axis, const int32_t* slot_map,
+                           int n_tokens, int Hq, int Hkv, int d, int rot_dim, int num_axes, int64_t pos_stride,
+                           int64_t q_stride, int64_t k_stride, int64_t v_stride, int adjacent, int block_size,
+                           int num_blocks, void* q_out, void* k_cache, void* v_cache, attn_stream_t stream);
+
+/*
+ * rope_axes_paged_append_fp8 - the same into an FP8 (e4m3) cache: the codes
+ * of k_rotated / k_scale and v / v_scale (fp32 quotients, round to nearest
+ * even, saturated to +-448; NaN stays NaN).
+ *   Supported: d == 128; otherwise as rope_axes_paged_append;
+ *   ATTN_ERR_INVALID_ARG also for a scale that is not finite and positive.
+ */
+int rope_axes_paged_append_fp8(const void* q, const void* k, const void* v, const int32_t* positions,
+                               const float* inv_freq, const uint8_t* freq_axis, const int32_t* slot_map,
+                               int n_tokens, int Hq, int Hkv, int d, int rot_dim, int num_axes,
+                               int64_t pos_stride, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                               int adjacent, int block_size, int num_blocks, float k_scale, float v_scale,
+                               void* q_out, void* k_cache, void* v_cache, attn_stream_t stream);
+
+/*
+ * paged_attn_prefill_fp8 - paged_attn_prefill over an FP8 (e4m3) cache with
+ * one scale per tensor (K = k_scale * k_cache, V = v_scale * v_cache), for
+ * chunks of any size down to one token per sequence.
+ *
+ *   k_cache, v_cache [num_blocks, 16, Hkv, 128] e4m3 bytes; num_splits: the
+ *   key range of each sequence is cut into at most num_splits ranges of whole
+ *   128-key tiles whose partial results are merged; <= 0 picks a value that
+ *   fills the GPU.  All other arguments and the result as paged_attn_prefill.
+ *   Output rows behind the last sequence (total_q > cu_seqlens_q[B]) are left
+ *   as they were.  Deterministic; the result does not depend on the blocks'
+ *   physical placement.
+ *
+ *   Rounding: q enters the score products as the sum of two e4m3 terms after
+ *   a power-of-two scaling of its row, which is exact for elements down to
+ *   2^-9 of the row's largest (2^-18 of the largest below); the weights are
+ *   rounded to f16 before they meet V; sums are fp32.  Cached values that a
+ *   sequence holds are assumed finite; slots past its end may hold anything.
+ *   Workspace: with more than one range, ranges * total_q * Hq * 129 fp32 from
+ *   the library's stream-ordered pool.
+ *   Supported: d == 128; block_size == 16; Hq / Hkv <= 128; max_blocks < 2^27;
+ *   16-byte aligned q, caches and o; sm_100.  Errors: as paged_attn_prefill;
+ *   ATTN_ERR_INVALID_ARG also for a k_scale or v_scale that is not finite and
+ *   positive.
+ */
+int paged_attn_prefill_fp8(const void* q, const void* k_cache, const void* v_cache,
+                           const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_seqlens_q,
+                           int B, int Hq, int Hkv, int d, int block_size, int max_blocks, int max_seqlen_q,
+                           int total_q, int causal, float scale, float k_scale, float v_scale, int num_splits,
+                           void* o, float* lse, attn_stream_t stream);
+
+/*
+ * paged_attn_prefill_fp8_checked - paged_attn_prefill_fp8 for a pool of known
+ * size num_blocks, with the block-id check of paged_attn_prefill_checked.
+ */
+int paged_attn_prefill_fp8_checked(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_table, const int32_t* seq_lens,
+                                   const int32_t* cu_seqlens_q, int B, int Hq, int Hkv, int d, int block_size,
+                                   int max_blocks, int num_blocks, int max_seqlen_q, int total_q, int causal,
+                                   float scale, float k_scale, float v_scale, int num_splits, void* o,
+                                   float* lse, attn_stream_t stream);
 
 #ifdef __cplusplus
 }
