@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(LIB_DIR, "libattn_b200.so")
 
 SOURCES = ["attn_api.cu"]
 HEADERS = ["sm100_ptx.cuh", "prefill_sm100.cuh", "decode_paged.cuh", "decode_paged_fp8.cuh", "paged_plan.cuh",
-           "rope_axes.cuh", "prefill_fp8_sm100.cuh"]
+           "rope_axes.cuh", "prefill_fp8_sm100.cuh", "prefill_fp8_few.cuh"]
 
 
 def nvcc_path() -> str:

@@ -15,6 +15,7 @@
 #include "decode_paged.cuh"
 #include "decode_paged_fp8.cuh"
 #include "paged_plan.cuh"
+#include "prefill_fp8_few.cuh"
 #include "prefill_fp8_sm100.cuh"
 #include "prefill_sm100.cuh"
 #include "rope_axes.cuh"
@@ -137,6 +138,8 @@ int prepare_device(int dev, DeviceState* st) {
       {reinterpret_cast<const void*>(decode::paged_decode_split<128>), decode::smem_bytes<128>()},
       {reinterpret_cast<const void*>(decode::paged_decode_split_fp8), decode::smem_bytes_fp8()},
       {reinterpret_cast<const void*>(prefill8::prefill_fp8_sm100), prefill8::smem_bytes()},
+      {reinterpret_cast<const void*>(prefill8::prefill_fp8_few<16>), prefill8::few_smem_bytes<16>()},
+      {reinterpret_cast<const void*>(prefill8::prefill_fp8_few<32>), prefill8::few_smem_bytes<32>()},
   };
   for (const auto& k : kernels)
     if (cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(k.bytes)) !=
@@ -1046,11 +1049,17 @@ int launch_prefill_fp8(const void* q, const void* kc, const void* vc, const int3
   const int G = Hq / Hkv;
   prefill8::Params p;
   std::memset(&p, 0, sizeof(p));
-  p.tok_tile = prefill8::kBM / G;
+  if (max_q > total_q) max_q = total_q;
+  // Sequences with few query rows (rows = new tokens x heads of a kv head)
+  // take the kernel with the rows on the MMA's columns.
+  const long long max_rows = static_cast<long long>(max_q) * G;
+  const int few = max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : 0;
+  p.tok_tile = (few ? few : prefill8::kBM) / G;
   CUtensorMap mq, mk, mv;
-  if (make_map_q_tile(&mq, q, total_q, Hq, G, p.tok_tile) ||
+  std::memset(&mq, 0, sizeof(mq));
+  if ((!few && make_map_q_tile(&mq, q, total_q, Hq, G, p.tok_tile)) ||
       make_map_pool_e4m3(&mk, kc, Hkv, num_blocks, CU_TENSOR_MAP_SWIZZLE_128B) ||
-      make_map_pool_e4m3(&mv, vc, Hkv, num_blocks, CU_TENSOR_MAP_SWIZZLE_NONE))
+      make_map_pool_e4m3(&mv, vc, Hkv, num_blocks, few ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE))
     return ATTN_ERR_CUDA;
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
@@ -1068,26 +1077,28 @@ int launch_prefill_fp8(const void* q, const void* kc, const void* vc, const int3
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * k_scale * 1.4426950408889634f;
   p.v_scale = v_scale;
-  const int rows_cta = 2 * p.tok_tile;
-  if (max_q > total_q) max_q = total_q;
+  const int rows_cta = (few ? 1 : 2) * p.tok_tile;
   p.num_mblocks = (max_q + rows_cta - 1) / rows_cta;
   long long items = static_cast<long long>(p.num_mblocks) * B;
-  if (B <= 32) {
+  if (!few && B <= 32) {
     const long long bound = (static_cast<long long>(total_q) + static_cast<long long>(B) * (rows_cta - 1)) / rows_cta;
     if (bound < items) items = bound;
     p.items = static_cast<int>(items);
   }
+  // Ranges of key tiles.  The host does not know the lengths, so a sequence
+  // counts as filling its table row.  Fewer units than resident CTAs: as many
+  // ranges as fill one wave.  A batch of few-row sequences: about three waves,
+  // so that unequal lengths even out.  No range under 4 tiles (512 keys).
   const int max_tiles = (max_blocks + 7) / 8;
-  long long chunk;
+  const long long units = items * Hkv, slots = static_cast<long long>(few ? prefill8::kFewCtasPerSm : 1) * st->sms;
+  long long splits = num_splits;
   if (num_splits <= 0) {
-    const long long waves = B == 1 ? 1 : 3;
-    chunk = (items * Hkv * max_tiles + waves * st->sms - 1) / (waves * st->sms);
-    if (chunk < 4) chunk = 4;
-  } else {
-    chunk = (max_tiles + num_splits - 1) / num_splits;
+    splits = units <= slots ? slots / units : 1;
+    if (few && B > 1) splits = (3 * slots + units - 1) / units;
+    if (splits > (max_tiles + 3) / 4) splits = (max_tiles + 3) / 4;
   }
-  if (chunk > max_tiles) chunk = max_tiles;
-  p.chunk = static_cast<int>(chunk);
+  if (splits > max_tiles) splits = max_tiles;
+  p.chunk = static_cast<int>((max_tiles + splits - 1) / splits);
   p.splits = (max_tiles + p.chunk - 1) / p.chunk;
   const long long grid = items * Hkv * p.splits;
   const long long merge_grid =
@@ -1113,8 +1124,14 @@ int launch_prefill_fp8(const void* q, const void* kc, const void* vc, const int3
     p.part_o = static_cast<float*>(ws);
     p.part_lse = p.part_o + rows * D;
   }
-  int rc = launch_pdl(prefill8::prefill_fp8_sm100, dim3(static_cast<unsigned>(grid)), dim3(prefill8::kThreads),
-                      prefill8::smem_bytes(), stream, mq, mk, mv, p);
+  const dim3 ctas(static_cast<unsigned>(grid));
+  const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(q);
+  int rc = few == 16   ? launch_pdl(prefill8::prefill_fp8_few<16>, ctas, dim3(prefill8::kFewThreads),
+                                    prefill8::few_smem_bytes<16>(), stream, mk, mv, qp, p)
+           : few == 32 ? launch_pdl(prefill8::prefill_fp8_few<32>, ctas, dim3(prefill8::kFewThreads),
+                                    prefill8::few_smem_bytes<32>(), stream, mk, mv, qp, p)
+                       : launch_pdl(prefill8::prefill_fp8_sm100, ctas, dim3(prefill8::kThreads),
+                                    prefill8::smem_bytes(), stream, mq, mk, mv, p);
   if (rc == ATTN_OK && p.splits > 1)
     rc = launch_pdl(prefill8::prefill_fp8_combine, dim3(static_cast<unsigned>(merge_grid)),
                     dim3(prefill8::kCombineWarps * 32), 0, stream, static_cast<const float*>(p.part_o),

@@ -114,6 +114,44 @@ __device__ __forceinline__ float2 f16x2_to_float2(uint32_t x) {
                      __half2float(__ushort_as_half(static_cast<unsigned short>(x >> 16))));
 }
 
+// Power-of-two scale of a query row whose largest magnitude has the bf16 bits
+// `top`: up brings it into [128, 256), down = 1 / up.  A row with NaN or
+// infinity gets down = NaN, and with it NaN scores.
+struct RowScale {
+  float up, down;
+};
+
+__device__ __forceinline__ RowScale row_scale(uint32_t top) {
+  const int ex = max(static_cast<int>(top >> 7) - 127, -110);  // keeps 2^(7 - ex) finite
+  RowScale s;
+  s.up = __int_as_float((7 - ex + 127) << 23);
+  s.down = ex == 128 ? __int_as_float(0x7fffffff) : __int_as_float((ex - 7 + 127) << 23);
+  return s;
+}
+
+// The row's factor from score to exponent; never 0, which times a masked -inf
+// would be NaN.
+__device__ __forceinline__ float row_score_scale(float scale_log2, const RowScale& rs) {
+  const float s = scale_log2 * rs.down;
+  return s < 1.2e-38f ? 1.2e-38f : s;  // false for NaN
+}
+
+// 16 bf16 elements, scaled, as e4m3 terms: hi = e4m3(x), lo = e4m3(x - hi).
+__device__ __forceinline__ void split_e4m3(const uint32_t (&w)[8], float up, uint4& hi, uint4& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x0 = __uint_as_float(w[2 * i] << 16) * up, x1 = __uint_as_float(w[2 * i] & 0xffff0000u) * up;
+    const float x2 = __uint_as_float(w[2 * i + 1] << 16) * up, x3 = __uint_as_float(w[2 * i + 1] & 0xffff0000u) * up;
+    const uint32_t h01 = pack_e4m3x2(x0, x1), h23 = pack_e4m3x2(x2, x3);
+    const float2 f01 = f16x2_to_float2(e4m3x2_to_f16x2(h01)), f23 = f16x2_to_float2(e4m3x2_to_f16x2(h23));
+    h[i] = h01 | (h23 << 16);
+    l[i] = pack_e4m3x2(x0 - f01.x, x1 - f01.y) | (pack_e4m3x2(x2 - f23.x, x3 - f23.y) << 16);
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
 // Key tiles that the tokens [t0, t0 + n) of a sequence see.
 __device__ __forceinline__ int key_tiles(int t0, int n, int T, int S, int causal) {
   if (t0 >= T) return 0;
@@ -345,6 +383,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // store their two 16-byte units in the other order, so that the eight
       // units of a store lie in different banks.
       const int u = lane & 7, c = u >> 2;
+      const int x = (warp - kWarpConv) * 4 + (lane >> 3);  // rows x, x + 8, ..
+      static_assert(kConvWarps == 2, "two warps take four rows of every eight each");
+      const int src_off = x * 128 + u * 16;
+      const int dst_a = c * static_cast<int>(kChunkBytes) + x * 128 + (((2 * (u & 3) + c) ^ x) << 4);
+      const int dst_b = c * static_cast<int>(kChunkBytes) + x * 128 + (((2 * (u & 3) + 1 - c) ^ x) << 4);
       bool ok = true;
       for (int j = 0; j < n_max; ++j) {
         const int sr = j % kVRaw, s = j % kVStages;
@@ -355,29 +398,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_done[it % kKStages], (it / kKStages) & 1, abort_flag));
           if (!ok) break;
         }
+        uint8_t* src = sm.v_raw[sr] + src_off;
+        uint8_t* dst = sm.v[s][0];
         const int valid = sm.v_valid[sr];
         const uint32_t bad = sm.v_bad[sr];
-        const bool whole = valid == kBN && bad == 0;
+        if (valid < kBN || bad != 0) {  // each lane clears the codes that it reads below
+          for (int i = 0; i < kBN / 8; ++i)
+            if (i * 8 + x >= valid || ((bad >> (i >> 1)) & 1u))
+              *reinterpret_cast<uint4*>(src + i * 1024) = make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
-        for (int part = 0; part < kBN / (kConvWarps * 16); ++part) {
+        for (int part = 0; part < kBN / 32; ++part) {
           uint4 raw[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = ((part * 4 + i) * kConvWarps + warp - kWarpConv) * 4 + (lane >> 3);
-            raw[i] = *reinterpret_cast<const uint4*>(sm.v_raw[sr] + row * 128 + u * 16);
-            if (!whole && (row >= valid || ((bad >> (row >> 4)) & 1u))) raw[i] = make_uint4(0u, 0u, 0u, 0u);
-          }
+          for (int i = 0; i < 4; ++i) raw[i] = *reinterpret_cast<const uint4*>(src + (part * 4 + i) * 1024);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int row = ((part * 4 + i) * kConvWarps + warp - kWarpConv) * 4 + (lane >> 3);
-            const uint4 lo = make_uint4(e4m3x2_to_f16x2(raw[i].x & 0xffffu), e4m3x2_to_f16x2(raw[i].x >> 16),
-                                        e4m3x2_to_f16x2(raw[i].y & 0xffffu), e4m3x2_to_f16x2(raw[i].y >> 16));
-            const uint4 hi = make_uint4(e4m3x2_to_f16x2(raw[i].z & 0xffffu), e4m3x2_to_f16x2(raw[i].z >> 16),
-                                        e4m3x2_to_f16x2(raw[i].w & 0xffffu), e4m3x2_to_f16x2(raw[i].w >> 16));
-            uint8_t* dst = sm.v[s][c] + row * 128;
-            const int unit = 2 * (u & 3);
-            *reinterpret_cast<uint4*>(dst + (((unit + c) ^ (row & 7)) << 4)) = c ? hi : lo;
-            *reinterpret_cast<uint4*>(dst + (((unit + 1 - c) ^ (row & 7)) << 4)) = c ? lo : hi;
+            const uint32_t a0 = c ? raw[i].z : raw[i].x, a1 = c ? raw[i].w : raw[i].y;
+            const uint32_t b0 = c ? raw[i].x : raw[i].z, b1 = c ? raw[i].y : raw[i].w;
+            *reinterpret_cast<uint4*>(dst + dst_a + (part * 4 + i) * 1024) =
+                make_uint4(e4m3x2_to_f16x2(a0 & 0xffffu), e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(a1 & 0xffffu),
+                           e4m3x2_to_f16x2(a1 >> 16));
+            *reinterpret_cast<uint4*>(dst + dst_b + (part * 4 + i) * 1024) =
+                make_uint4(e4m3x2_to_f16x2(b0 & 0xffffu), e4m3x2_to_f16x2(b0 >> 16), e4m3x2_to_f16x2(b1 & 0xffffu),
+                           e4m3x2_to_f16x2(b1 >> 16));
           }
         }
         fence_proxy_async_smem();  // the generic writes before the tensor core reads the tile
@@ -418,32 +462,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             w[c * 32 + u * 4] = x.x, w[c * 32 + u * 4 + 1] = x.y, w[c * 32 + u * 4 + 2] = x.z,
                            w[c * 32 + u * 4 + 3] = x.w;
           }
-        uint32_t top = 0;  // largest magnitude, as bf16 bits (NaN and infinity on top)
+        uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 64; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
-        top = max(top & 0xffffu, top >> 16);
-        int ex = static_cast<int>(top >> 7) - 127;
-        if (!row_real) ex = 0;
-        if (ex == 128) sl2 = __int_as_float(0x7fffffff);  // the row's scores are NaN
-        ex = max(ex, -110);  // keeps 2^(7 - ex) finite
-        const float up = __int_as_float((7 - ex + 127) << 23);
-        sl2 *= __int_as_float((ex - 7 + 127) << 23);
+        const RowScale rs = row_scale(row_real ? max(top & 0xffffu, top >> 16) : 0);
+        sl2 = row_score_scale(sl2, rs);
 #pragma unroll
         for (int u = 0; u < 8; ++u) {  // 16 elements: one 16-byte unit of each term
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t a = w[u * 8 + 2 * i], bq = w[u * 8 + 2 * i + 1];
-            const float x0 = __uint_as_float(a << 16) * up, x1 = __uint_as_float(a & 0xffff0000u) * up;
-            const float x2 = __uint_as_float(bq << 16) * up, x3 = __uint_as_float(bq & 0xffff0000u) * up;
-            const uint32_t h01 = pack_e4m3x2(x0, x1), h23 = pack_e4m3x2(x2, x3);
-            const float2 f01 = f16x2_to_float2(e4m3x2_to_f16x2(h01));
-            const float2 f23 = f16x2_to_float2(e4m3x2_to_f16x2(h23));
-            hi[i] = h01 | (h23 << 16);
-            lo[i] = pack_e4m3x2(x0 - f01.x, x1 - f01.y) | (pack_e4m3x2(x2 - f23.x, x3 - f23.y) << 16);
-          }
-          *reinterpret_cast<uint4*>(sm.q[t][0] + r * 128 + ((u ^ sw) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(sm.q[t][1] + r * 128 + ((u ^ sw) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          uint4 hi, lo;
+          split_e4m3(*reinterpret_cast<uint32_t(*)[8]>(&w[u * 8]), rs.up, hi, lo);
+          *reinterpret_cast<uint4*>(sm.q[t][0] + r * 128 + ((u ^ sw) << 4)) = hi;
+          *reinterpret_cast<uint4*>(sm.q[t][1] + r * 128 + ((u ^ sw) << 4)) = lo;
         }
         fence_proxy_async_smem();
         __syncwarp();

@@ -304,6 +304,13 @@ __device__ __forceinline__ uint64_t make_sdesc_sw128(uint32_t saddr, uint32_t lb
   return d;
 }
 
+// The same with any swizzle: layout 2 = 128-byte, 4 = 64-byte, 6 = 32-byte.
+__device__ __forceinline__ uint64_t make_sdesc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes,
+                                               uint64_t layout) {
+  return uint64_t((saddr >> 4) & 0x3FFFu) | uint64_t((lbo_bytes >> 4) & 0x3FFFu) << 16 |
+         uint64_t((sbo_bytes >> 4) & 0x3FFFu) << 32 | 1ull << 46 | layout << 61;
+}
+
 // Tensor-memory loads.  Warp w may only touch lanes 32*(w%4)..32*(w%4)+31;
 // taddr = base + (lane_offset << 16) + column.  The wait::ld is part of the
 // same asm statement, so no use of the destination registers can be
