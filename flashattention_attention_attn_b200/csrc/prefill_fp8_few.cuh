@@ -8,18 +8,22 @@
 // longer than the tile's bytes.  Here the products are turned round, keys and
 // head dim on the 128 lanes and the rows on the columns:
 //   S^T [128 keys x 2R] = K [keys x d] (Q_hi ; Q_lo)^T
-//   O^T [128 d x 2R]   += V^T [d x keys] (P_hi ; P_lo)
+//   O^T [128 d x 4R]   += V^T [d x keys] (P_0 ; P_1 ; P_2 ; P_3)
 // K and V go to the 8-bit MMAs as the e4m3 codes they are (V read transposed),
 // nothing is converted, and a thread owns one key: R exponentials a tile.
 //
 // q is split into two e4m3 terms as in the other kernel; both stand side by
 // side in the N dimension of one MMA and a thread adds its two columns.  The
-// weights are split the same way, P_hi = e4m3(p), P_lo = e4m3(p - P_hi): 8
-// significant bits, as bf16 weights have.  e4m3's range is short (its smallest
-// step is 2^-9), so p = 2^(x - m + 7) with m within 1 of the running maximum:
-// p <= 2^8, and a weight of 2^-8 of the largest still has its 8 bits.
+// weights are rounded to f16 and split exactly into four e5m2 terms (an e5m2
+// number is the top byte of an f16: each term takes three of the eleven bits
+// left, the rest is the exact f16 difference); the four products are added at
+// the end.  Two e4m3 terms would need half the columns, but their smallest step
+// of 2^-9 leaves few bits to weights far below the row's largest one, and a
+// long row can hold most of its sum in those.  e5m2 reaches 2^-16: with
+// p = 2^(x - m + 7) and m within 8 of the running maximum, p lies in (0, 2^15]
+// and weights keep their bits down to 2^-20 of the largest.
 //
-// The reference m of a row moves only when a score exceeds it by more than 1:
+// The reference m of a row moves only when a score exceeds it by more than 8:
 // the four softmax warps vote on that with one barrier a tile and only then
 // reduce the maxima over the keys and rescale O^T.  Row sums stay in the
 // threads until the end.
@@ -38,17 +42,18 @@ namespace prefill8 {
 constexpr int kFewThreads = 192;
 constexpr int kFewCtasPerSm = 2;
 constexpr float kFewShift = 7.0f;  // p = 2^(x - m + 7)
-constexpr float kFewLimit = 8.0f;  // exponents above this move m
+constexpr float kFewLimit = 15.0f;  // exponents above this move m
 constexpr float kFewUnseen = 1e30f;  // offset of a row that has seen no key
 
 template <int R>
 struct FewConfig {
-  static constexpr int kN = 2 * R;                             // MMA columns
-  static constexpr int kSlots = R <= 16 ? 6 : 5;               // ring of 16 KB tiles
-  static constexpr uint32_t kTmem = R <= 16 ? 128 : 256;       // columns: 2 S^T buffers + O^T = 6R
-  static constexpr uint32_t kPBytes = kBN * kN;                // P_hi, P_lo of one tile
-  // P rows (one per key) are kN bytes: 32- or 64-byte swizzle
-  static constexpr uint64_t kPLayout = kN == 32 ? 6 : 4;
+  static constexpr int kN = 2 * R;                             // columns of S^T
+  static constexpr int kNP = 4 * R;                            // columns of O^T
+  static constexpr int kSlots = R <= 16 ? 5 : 4;               // ring of 16 KB tiles
+  static constexpr uint32_t kTmem = 8 * R;                     // columns: 2 S^T buffers + O^T
+  static constexpr uint32_t kPBytes = kBN * kNP;               // the terms of one tile's weights
+  // P rows (one per key) are kNP bytes: 64- or 128-byte swizzle
+  static constexpr uint64_t kPLayout = kNP == 64 ? 4 : 2;
 };
 
 template <int R>
@@ -83,6 +88,12 @@ __device__ __forceinline__ bool vote_or_128(bool pred) {
       : "r"(pred ? 1u : 0u)
       : "memory");
   return r != 0;
+}
+
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 template <int COLS>
@@ -201,7 +212,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
     // ----------------------------- MMA issuer -----------------------------
     if (lane == 0) {
       constexpr uint32_t idesc_qk = make_idesc_fmt0(128, C::kN, 0, 0);  // K, (Q_hi ; Q_lo): head dim contiguous
-      constexpr uint32_t idesc_pv = make_idesc_fmt0(128, C::kN, 1, 1);  // V, (P_hi ; P_lo): keys apart
+      // V (e4m3), P (e5m2: format 1 of B), both with the keys apart
+      constexpr uint32_t idesc_pv = make_idesc_fmt0(128, C::kNP, 1, 1) | 1u << 10;
       bool ok = mbar_wait(&sm.q_ready, 0, abort_flag);
       tc_fence_after();
       const uint32_t qbase = smem_u32(sm.q);
@@ -230,7 +242,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)  // 32 keys at a time
           umma_ss_f8(tmem + 2 * C::kN, make_sdesc_sw128(vbase + kk * 32 * 128, 16, 1024),
-                     make_sdesc(pbase + kk * 32 * C::kN, 16, 8 * C::kN, C::kPLayout), idesc_pv,
+                     make_sdesc(pbase + kk * 32 * C::kNP, 16, 8 * C::kNP, C::kPLayout), idesc_pv,
                      (j > 0 || kk > 0) ? 1u : 0u);
         umma_commit(&sm.p_free[buf]);
         umma_commit(&sm.empty[s]);
@@ -346,7 +358,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
           if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free[buf ^ 1], ((j - 1) >> 1) & 1, abort_flag));
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < C::kN / 32; ++c) {
+          for (int c = 0; c < C::kNP / 32; ++c) {
             uint32_t u[32];
             tmem_ld32_sync(tO + c * 32, u);
 #pragma unroll
@@ -362,7 +374,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
           y[r] = fmaf(x[r], sm.sl2[r], sm.off[r]);
         }
       }
-      uint32_t hi[R / 4], lo[R / 4];
+      uint32_t pt[4][R / 4];  // the weights' e5m2 terms, four rows to a word
 #pragma unroll
       for (int r = 0; r < R; r += 4) {
         const float p0 = ex2_approx(y[r]), p1 = ex2_approx(y[r + 1]), p2 = ex2_approx(y[r + 2]),
@@ -371,21 +383,26 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
         l[r + 1] += p1;
         l[r + 2] += p2;
         l[r + 3] += p3;
-        const uint32_t h01 = pack_e4m3x2(p0, p1), h23 = pack_e4m3x2(p2, p3);
-        const float2 f01 = f16x2_to_float2(e4m3x2_to_f16x2(h01)), f23 = f16x2_to_float2(e4m3x2_to_f16x2(h23));
-        hi[r / 4] = h01 | (h23 << 16);
-        lo[r / 4] = pack_e4m3x2(p0 - f01.x, p1 - f01.y) | (pack_e4m3x2(p2 - f23.x, p3 - f23.y) << 16);
+        uint32_t a = pack_f16x2(p0, p1), c = pack_f16x2(p2, p3);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          pt[t][r / 4] = prmt(a, c, 0x7531);  // the four top bytes
+          if (t < 3) {
+            a = hsub2(a, a & 0xff00ff00u);
+            c = hsub2(c, c & 0xff00ff00u);
+          }
+        }
       }
       if (ok && j >= 2)  // the P buffer's last reader: the tile two before
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free[buf], ((j - 2) >> 1) & 1, abort_flag));
-      const int sw = C::kN == 32 ? (k >> 2) & 1 : (k >> 1) & 3;
-      uint8_t* prow = sm.p[buf] + k * C::kN;
+      const int sw = C::kNP == 64 ? (k >> 1) & 3 : k & 7;
+      uint8_t* prow = sm.p[buf] + k * C::kNP;
 #pragma unroll
-      for (int u = 0; u < R / 16; ++u) {
-        *reinterpret_cast<uint4*>(prow + ((u ^ sw) << 4)) = make_uint4(hi[4 * u], hi[4 * u + 1], hi[4 * u + 2], hi[4 * u + 3]);
-        *reinterpret_cast<uint4*>(prow + (((R / 16 + u) ^ sw) << 4)) =
-            make_uint4(lo[4 * u], lo[4 * u + 1], lo[4 * u + 2], lo[4 * u + 3]);
-      }
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int u = 0; u < R / 16; ++u)
+          *reinterpret_cast<uint4*>(prow + (((t * (R / 16) + u) ^ sw) << 4)) =
+              make_uint4(pt[t][4 * u], pt[t][4 * u + 1], pt[t][4 * u + 2], pt[t][4 * u + 3]);
       if (__any_sync(0xffffffffu, dead)) {
         // no weight falls on this key, but its V row may hold anything (NaN codes): cleared before the MMA reads it
         const int i = 2 * j + 1;
@@ -428,13 +445,21 @@ __global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
     if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_full, 0, abort_flag));
     if (ok) {
       tc_fence_after();
-      uint32_t u[C::kN];
-      tmem_load_cols<C::kN>(tO, u);
+      float sum[R];  // the four terms' products
+      {
+        uint32_t u[2 * R], v[2 * R];
+        tmem_load_cols<2 * R>(tO, u);
+        tmem_load_cols<2 * R>(tO + 2 * R, v);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          sum[r] = (__uint_as_float(u[r]) + __uint_as_float(u[R + r])) +
+                   (__uint_as_float(v[r]) + __uint_as_float(v[R + r]));
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const size_t tok = static_cast<size_t>(qoff) + r / p.G;
         if (r < rows && tok < static_cast<size_t>(p.total_q)) {
-          const float o = (__uint_as_float(u[r]) + __uint_as_float(u[R + r])) * sm.alpha[r];
+          const float o = sum[r] * sm.alpha[r];
           const size_t row = tok * p.Hq + hk * p.G + r % p.G;
           if (p.splits > 1)
             p.part_o[(static_cast<size_t>(split) * p.total_q * p.Hq + row) * kD + k] = o;

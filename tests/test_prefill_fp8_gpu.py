@@ -161,8 +161,9 @@ def test_more_queries_than_keys_and_no_keys():
             check(*a[:3], causal, a[3], o, lse)
 
 
-def test_placement_and_garbage_past_the_end():
-    q, cu, c, scale = make([37, 300, 1000, 16], [5, 300, 70, 16], seed=75)
+@pytest.mark.parametrize("ql", [[5, 300, 70, 16], [4, 1, 3, 4], [8, 7, 1, 2]])
+def test_placement_and_garbage_past_the_end(ql):
+    q, cu, c, scale = make([37, 300, 1000, 16], ql, seed=75)
     for splits in (1, 2):
         want = run(q, cu, c, True, scale, splits=splits)
         g = torch.Generator().manual_seed(9)
@@ -181,8 +182,9 @@ def test_placement_and_garbage_past_the_end():
         assert torch.equal(again[0], want[0])
 
 
-def test_ids_outside_the_pool_and_lengths_past_the_row():
-    q, cu, c, scale = make([500, 300, 64], [40, 300, 3], seed=21, spare=40)
+@pytest.mark.parametrize("ql", [[40, 300, 3], [4, 2, 3], [8, 1, 5]])
+def test_ids_outside_the_pool_and_lengths_past_the_row(ql):
+    q, cu, c, scale = make([500, 300, 64], ql, seed=21, spare=40)
     pool = c.k_cache.shape[0] - 20  # the last blocks stay inside the allocation
     t = c.block_table.clone()
     t[0, 3], t[0, 30], t[1, 0], t[1, 18] = -1, pool + 3, pool, 1 << 30
@@ -205,21 +207,23 @@ def test_ids_outside_the_pool_and_lengths_past_the_row():
     check(q, cu, f, True, scale, o, lse)
 
 
+@pytest.mark.parametrize("T", [70, 3, 8])
 @pytest.mark.parametrize("factor", [2.0 ** -100, 2.0 ** -20, 1.0, 2.0 ** 40])
-def test_any_size_of_query(factor):
+def test_any_size_of_query(factor, T):
     """Rows are scaled by powers of two inside; with the score scale undone outside the result is the same."""
-    q, cu, c, scale = make([200, 90], [70, 1], Hq=8, Hkv=2, seed=5)
+    q, cu, c, scale = make([200, 90], [T, 1], Hq=8, Hkv=2, seed=5)
     base = run(q, cu, c, True, scale)
     big = run((q.float() * factor).to(torch.bfloat16), cu, c, True, scale / factor)
     assert torch.equal(big[0], base[0]) and torch.allclose(big[1], base[1], rtol=1e-6, atol=1e-6)
 
 
-def test_uneven_rows_and_rising_scores():
+@pytest.mark.parametrize("ql", [[300, 2], [4, 3], [8, 5]])
+def test_uneven_rows_and_rising_scores(ql):
     """One element far above the rest of its row, rows of zeros, and keys that grow along the sequence, so that the
     running maximum moves many times."""
-    q, cu, c, scale = make([900, 700], [300, 2], seed=6)
+    q, cu, c, scale = make([900, 700], ql, seed=6)
     q[::3, :, 5] *= 300.0
-    q[7] = 0.0
+    q[1] = 0.0
     codes = torch.arange(16 * c.k_cache.shape[0]) % 100  # a code that rises through each block
     c.k_cache[..., 9] = codes.view(-1, 16, 1).to(torch.uint8)
     for splits in (1, 4):
@@ -228,15 +232,16 @@ def test_uneven_rows_and_rising_scores():
         check(q, cu, c, True, scale, o, lse)
 
 
-def test_nan_query_row_stays_alone():
-    q, cu, c, scale = make([300], [300], Hq=8, Hkv=2, seed=31)
-    want = run(q, cu, c, True, scale)
+@pytest.mark.parametrize("T", [300, 4, 8])
+def test_nan_query_row_stays_alone(T):
+    q, cu, c, scale = make([300], [T], Hq=8, Hkv=2, seed=31)
+    want = run(q, cu, c, True, scale, splits=1)
     q2 = q.clone()
-    q2[100, 3, 7], q2[200, 1, 0] = float("nan"), float("inf")
+    q2[T // 3, 3, 7], q2[2 * T // 3, 1, 0] = float("nan"), float("inf")
     for splits in (1, 2):
         got = run(q2, cu, c, True, scale, splits=splits)
-        hit = torch.zeros(300, 8, dtype=torch.bool)
-        hit[100, 3] = hit[200, 1] = True
+        hit = torch.zeros(T, 8, dtype=torch.bool)
+        hit[T // 3, 3] = hit[2 * T // 3, 1] = True
         assert torch.isnan(got[0][hit]).all() and torch.isnan(got[1].t()[hit]).all()
         ref = want if splits == 1 else run(q, cu, c, True, scale, splits=2)
         assert torch.equal(got[0][~hit], ref[0][~hit]) and torch.equal(got[1].t()[~hit], ref[1].t()[~hit])
@@ -247,6 +252,26 @@ def test_long_cache_few_rows():
     o, lse, st = run(*a[:3], False, a[3])
     assert st == 0
     check(*a[:3], False, a[3], o, lse)
+
+
+@pytest.mark.parametrize("T", [2, 8, 40])
+def test_most_of_the_sum_in_small_weights(T):
+    """One key far above all others (an attention sink) before thousands whose weights are 2^-13 of its: together they
+    outweigh it, so the small weights' bits decide the result."""
+    S, Hkv = 16000, 1
+    q, cu, c, _ = make([S], [T], Hq=4, Hkv=Hkv, seed=90, k_scale=1.0)
+    q[:] = 1.0
+    c.k_cache[:] = 0
+    first = int(c.block_table[0, 0])
+    c.k_cache[first, 0, 0, :72] = 0x38  # 72 ones: a score of 9
+    rest = torch.randint(0, 3, c.k_cache.shape[:3], generator=torch.Generator().manual_seed(2)).to(torch.uint8)
+    c.k_cache[..., 127] += rest * 8  # small spread among the others
+    c.v_cache[:] = 0x38  # values of one: o is the sum of the rounded weights over the sum of the weights
+    c.v_cache[first, 0] = 0
+    for splits in (1, 4):
+        o, lse, st = run(q, cu, c, False, 0.125 * 8, splits=splits)
+        assert st == 0
+        check(q, cu, c, False, 0.125 * 8, o, lse)
 
 
 def test_two_streams_and_a_captured_call():
