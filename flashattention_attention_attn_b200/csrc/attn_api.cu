@@ -1041,6 +1041,67 @@ int make_map_pool_e4m3(CUtensorMap* map, const void* base, int Hkv, int num_bloc
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
+// Stream-ordered workspace: from the library's pool, or inside a stream
+// capture from cudaMallocAsync, which becomes a graph memory node.
+int workspace(void** ws, size_t bytes, cudaStream_t stream, const DeviceState* st) {
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
+    cudaGetLastError();
+    return ATTN_ERR_CUDA;
+  }
+  const cudaError_t e = cap == cudaStreamCaptureStatusActive ? cudaMallocAsync(ws, bytes, stream)
+                                                             : cudaMallocFromPoolAsync(ws, bytes, st->pool, stream);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return ATTN_ERR_CUDA;
+  }
+  return ATTN_OK;
+}
+
+// Few query rows per sequence.  num_splits <= 0: the tiles of all sequences
+// are dealt out evenly to one wave of CTAs.  Otherwise every sequence counts as
+// max_tiles long and each group of CTAs takes one of its num_splits ranges.
+template <int R>
+int launch_prefill_fp8_few(const CUtensorMap& mk, const CUtensorMap& mv, const void* q, const prefill8::Params& p,
+                           int max_tiles, int num_splits, cudaStream_t stream, const DeviceState* st) {
+  prefill8::FewParams f;
+  std::memset(&f, 0, sizeof(f));
+  f.p = p;
+  const long long units = static_cast<long long>(p.B) * p.Hkv;
+  long long groups;  // of p.Hkv CTAs
+  if (num_splits > 0) {
+    f.chunk = (max_tiles + num_splits - 1) / num_splits;
+    const int splits = (max_tiles + f.chunk - 1) / f.chunk;
+    f.seq_tiles = splits * f.chunk;
+    groups = static_cast<long long>(p.B) * splits;
+  } else {
+    const long long most = (static_cast<long long>(p.B) * (max_tiles + prefill8::kFewPieceCost) +
+                            prefill8::kFewMinChunk - 1) / prefill8::kFewMinChunk;
+    groups = prefill8::FewConfig<R>::kCtas * st->sms / p.Hkv;
+    if (groups < 1) groups = 1;
+    if (groups > most) groups = most;
+  }
+  const long long grid = groups * p.Hkv;
+  if (grid > 0x3fffffffLL || units > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  const size_t slots = static_cast<size_t>(grid) * 2;
+  void* ws = nullptr;
+  if (int rc = workspace(&ws, slots * R * (prefill8::kD + 1) * sizeof(float) + p.B * sizeof(int2), stream, st))
+    return rc;
+  f.part_o = static_cast<float*>(ws);
+  f.part_lse = f.part_o + slots * R * prefill8::kD;
+  f.meta = reinterpret_cast<int2*>(f.part_lse + slots * R);
+  int rc = launch_pdl(prefill8::prefill_fp8_few<R>, dim3(static_cast<unsigned>(grid)), dim3(prefill8::FewConfig<R>::kThreads),
+                      prefill8::few_smem_bytes<R>(), stream, mk, mv, static_cast<const __nv_bfloat16*>(q), f);
+  if (rc == ATTN_OK && num_splits != 1) {
+    const unsigned n = static_cast<unsigned>(units);
+    // few units are cut into many pieces: more warps on a row
+    rc = units * R <= 2048 ? launch_pdl(prefill8::prefill_fp8_few_merge<R, 1>, dim3(n, R), dim3(128), 0, stream, f)
+                           : launch_pdl(prefill8::prefill_fp8_few_merge<R, 4>, dim3(n, R / 4), dim3(128), 0, stream, f);
+  }
+  cudaFreeAsync(ws, stream);
+  return rc;
+}
+
 int launch_prefill_fp8(const void* q, const void* kc, const void* vc, const int32_t* table, const int32_t* lens,
                        const int32_t* cu_q, void* o, float* lse, int B, int max_q, int total_q, int Hq, int Hkv,
                        int max_blocks, int num_blocks, int causal, float scale, float k_scale, float v_scale,
@@ -1077,30 +1138,31 @@ int launch_prefill_fp8(const void* q, const void* kc, const void* vc, const int3
   p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * k_scale * 1.4426950408889634f;
   p.v_scale = v_scale;
-  const int rows_cta = (few ? 1 : 2) * p.tok_tile;
+  const int max_tiles = (max_blocks + 7) / 8;
+  if (num_splits > max_tiles) num_splits = max_tiles;
+  if (few)
+    return few == 16 ? launch_prefill_fp8_few<16>(mk, mv, q, p, max_tiles, num_splits, stream, st)
+                     : launch_prefill_fp8_few<32>(mk, mv, q, p, max_tiles, num_splits, stream, st);
+  const int rows_cta = 2 * p.tok_tile;
   p.num_mblocks = (max_q + rows_cta - 1) / rows_cta;
   long long items = static_cast<long long>(p.num_mblocks) * B;
-  if (!few && B <= 32) {
+  if (B <= 32) {
     const long long bound = (static_cast<long long>(total_q) + static_cast<long long>(B) * (rows_cta - 1)) / rows_cta;
     if (bound < items) items = bound;
     p.items = static_cast<int>(items);
   }
-  // Ranges of key tiles.  The host does not know the lengths, so a sequence
-  // counts as filling its table row.  Fewer units than resident CTAs: as many
-  // ranges as fill one wave.  A batch of few-row sequences: about three waves,
-  // so that unequal lengths even out.  No range under 4 tiles (512 keys).
-  const int max_tiles = (max_blocks + 7) / 8;
-  const long long units = items * Hkv, slots = static_cast<long long>(few ? prefill8::kFewCtasPerSm : 1) * st->sms;
+  // Ranges of key tiles: with fewer units than SMs, as many as fill one wave
+  // when every sequence fills its table row (the host does not know the
+  // lengths).  No range under 4 tiles (512 keys).
+  const long long units = items * Hkv;
   long long splits = num_splits;
   if (num_splits <= 0) {
-    splits = units <= slots ? slots / units : 1;
-    if (few && B > 1) splits = (3 * slots + units - 1) / units;
+    splits = units < st->sms ? st->sms / units : 1;
     if (splits > (max_tiles + 3) / 4) splits = (max_tiles + 3) / 4;
   }
-  if (splits > max_tiles) splits = max_tiles;
   p.chunk = static_cast<int>((max_tiles + splits - 1) / splits);
   p.splits = (max_tiles + p.chunk - 1) / p.chunk;
-  const long long grid = items * Hkv * p.splits;
+  const long long grid = units * p.splits;
   const long long merge_grid =
       (static_cast<long long>(total_q) * Hq + prefill8::kCombineWarps - 1) / prefill8::kCombineWarps;
   if (grid > 0x7fffffffLL || merge_grid > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
@@ -1108,30 +1170,12 @@ int launch_prefill_fp8(const void* q, const void* kc, const void* vc, const int3
   void* ws = nullptr;
   if (p.splits > 1) {
     const size_t rows = static_cast<size_t>(p.splits) * total_q * Hq;
-    const size_t bytes = rows * (D + 1) * sizeof(float);
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) {
-      cudaGetLastError();
-      return ATTN_ERR_CUDA;
-    }
-    const cudaError_t ae = (cap == cudaStreamCaptureStatusActive)
-                               ? cudaMallocAsync(&ws, bytes, stream)
-                               : cudaMallocFromPoolAsync(&ws, bytes, st->pool, stream);
-    if (ae != cudaSuccess) {
-      cudaGetLastError();
-      return ATTN_ERR_CUDA;
-    }
+    if (int rc = workspace(&ws, rows * (D + 1) * sizeof(float), stream, st)) return rc;
     p.part_o = static_cast<float*>(ws);
     p.part_lse = p.part_o + rows * D;
   }
-  const dim3 ctas(static_cast<unsigned>(grid));
-  const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(q);
-  int rc = few == 16   ? launch_pdl(prefill8::prefill_fp8_few<16>, ctas, dim3(prefill8::kFewThreads),
-                                    prefill8::few_smem_bytes<16>(), stream, mk, mv, qp, p)
-           : few == 32 ? launch_pdl(prefill8::prefill_fp8_few<32>, ctas, dim3(prefill8::kFewThreads),
-                                    prefill8::few_smem_bytes<32>(), stream, mk, mv, qp, p)
-                       : launch_pdl(prefill8::prefill_fp8_sm100, ctas, dim3(prefill8::kThreads),
-                                    prefill8::smem_bytes(), stream, mq, mk, mv, p);
+  int rc = launch_pdl(prefill8::prefill_fp8_sm100, dim3(static_cast<unsigned>(grid)), dim3(prefill8::kThreads),
+                      prefill8::smem_bytes(), stream, mq, mk, mv, p);
   if (rc == ATTN_OK && p.splits > 1)
     rc = launch_pdl(prefill8::prefill_fp8_combine, dim3(static_cast<unsigned>(merge_grid)),
                     dim3(prefill8::kCombineWarps * 32), 0, stream, static_cast<const float*>(p.part_o),

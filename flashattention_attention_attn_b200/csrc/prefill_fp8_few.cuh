@@ -24,14 +24,26 @@
 // and weights keep their bits down to 2^-20 of the largest.
 //
 // The reference m of a row moves only when a score exceeds it by more than 8:
-// the four softmax warps vote on that with one barrier a tile and only then
-// reduce the maxima over the keys and rescale O^T.  Row sums stay in the
-// threads until the end.
+// the four softmax warps note it and arrive on a barrier, make their
+// exponentials, and only then look whether one of them did; if so the maxima
+// over the keys are reduced, O^T is rescaled and the tile is done again.  Row
+// sums stay in the threads until the end.
 //
-// CTA = 6 warps: 0-3 softmax (thread k = key k of the tile = lane k), 4 copies
-// (a ring of 16 KB tiles, K and V in turn), 5 MMA issue; two CTAs to an SM.
-// S^T and P are double-buffered, so copies, both products and the softmax of
+// CTA: one softmax warpgroup for every 16 rows (thread k = key k of the tile =
+// lane k), a warp for the copies (a ring of 16 KB tiles, K and V in turn) and
+// one that issues the MMAs in the order in which they become ready; two CTAs to
+// an SM.  S^T is double-buffered, so copies, both products and the softmax of
 // neighbouring tiles run at the same time.
+//
+// Work split.  The sequences lie one behind the other on a line of key tiles.
+// A group of Hkv CTAs, one for each kv head, takes a stretch of the line, every
+// group the same length whatever the sequences' lengths are, and works through
+// the pieces of sequences on it (the copies run ahead into the next piece).  The
+// heads of a token lie side by side in the pool, 128 bytes each, so it matters
+// that a group's CTAs read them at about the same time.  A (sequence, kv head)
+// that lies on one stretch is finished there; the pieces of one that a stretch's
+// end cuts go to the workspace (at most two a CTA) and prefill_fp8_few_merge
+// joins them.
 #pragma once
 
 #include "prefill_fp8_sm100.cuh"
@@ -39,16 +51,22 @@
 namespace attn {
 namespace prefill8 {
 
-constexpr int kFewThreads = 192;
-constexpr int kFewCtasPerSm = 2;
+constexpr int kFewMinChunk = 4;    // length of a stretch at least
+// Length that a sequence adds to its tiles on the line: a piece's q, its first tile
+// (which sets the references) and its end take about as long as three tiles.
+constexpr int kFewPieceCost = 3;
 constexpr float kFewShift = 7.0f;  // p = 2^(x - m + 7)
 constexpr float kFewLimit = 15.0f;  // exponents above this move m
 constexpr float kFewUnseen = 1e30f;  // offset of a row that has seen no key
 
 template <int R>
 struct FewConfig {
+  static constexpr int kCtas = 2;                              // to an SM
+  static constexpr int kSoftmaxWarps = R / 4;                  // a warpgroup for every 16 rows
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + 2);
   static constexpr int kN = 2 * R;                             // columns of S^T
   static constexpr int kNP = 4 * R;                            // columns of O^T
+  static constexpr int kWgs = R / 16;
   static constexpr int kSlots = R <= 16 ? 5 : 4;               // ring of 16 KB tiles
   static constexpr uint32_t kTmem = 8 * R;                     // columns: 2 S^T buffers + O^T
   static constexpr uint32_t kPBytes = kBN * kNP;               // the terms of one tile's weights
@@ -56,39 +74,105 @@ struct FewConfig {
   static constexpr uint64_t kPLayout = kNP == 64 ? 4 : 2;
 };
 
+// A piece of a sequence, as the copy warp hands it to the others.
+struct FewPiece {
+  int b;                // sequence, -1: no more pieces
+  int j0, n;            // first tile, tiles
+  int qoff, T, S;
+  int whole, last;      // the whole sequence; its end
+  int g0;               // last: the group where it began
+};
+constexpr int kFewPieces = 2;  // the piece at work and the next one
+constexpr int kFewBad = 8;     // tiles whose bad-block bits are kept: more than the ring holds and S^T is ahead
+
 template <int R>
 struct __align__(1024) FewSmem {
   using C = FewConfig<R>;
   uint8_t ring[C::kSlots][kTile8];
-  uint8_t q[2 * R * kD];            // hi rows, then lo rows, 128-byte swizzle
-  uint8_t p[2][C::kPBytes];
-  float sl2[R];                     // score scale of each row, log2 domain
-  float off[R];                     // 7 - m
-  float alpha[R];
-  float red[4][R];
-  int lim[R];                       // last key position that the row sees
+  uint8_t q[kFewPieces][2 * R * kD];  // hi rows, then lo rows, 128-byte swizzle
+  uint8_t p[C::kPBytes];
+  FewPiece piece[kFewPieces];
+  alignas(16) float sl2[kFewPieces][R];  // score scale of each row, log2 domain (read four at a time)
+  int lim[kFewPieces][R];           // last key position that the row sees
+  // per softmax warp, for its warpgroup's 16 rows (every warp keeps its own copy):
+  alignas(16) float off[C::kSoftmaxWarps][16];  // 7 - m (read four at a time)
+  float alpha[C::kSoftmaxWarps][16];  // factor of a moved reference; v_scale / l at the end
+  float top[C::kSoftmaxWarps][16];    // maxima over the warp's keys
+  float sum[C::kSoftmaxWarps][16];    // row sums over the warp's keys
   uint64_t full[C::kSlots], empty[C::kSlots];
-  uint64_t q_ready, s_full[2], s_free[2], p_full[2], p_free[2], o_full;
+  uint64_t piece_full[kFewPieces], piece_free[kFewPieces];
+  uint64_t s_full[2], s_free[2], p_full, p_free, o_full, o_free, mma_done;
+  uint64_t vote[C::kWgs], sync[C::kWgs];
+  int moved[C::kWgs];               // last tile with a score that moves a reference
+  uint32_t bad[kFewBad];            // blocks of a tile outside the pool
+  long long chunk, begin, end, rest;  // the CTA's stretch; length into its first sequence
+  int b0;                           // that sequence
   uint32_t tmem_base;
   int abort_flag;
 };
 
+struct FewParams {
+  Params p;        // o, lse, cu_q, block_table, seq_lens, sizes, scales; tok_tile = R / G
+  float* part_o;   // [2 * CTAs][R][128]: pieces of cut sequences
+  float* part_lse; // [2 * CTAs][R]
+  int2* meta;      // [B]: first and last group of the sequence, equal when nothing is to be merged
+  int chunk;       // length of a group's stretch; 0: the line dealt out evenly
+  int seq_tiles;   // length of every sequence; 0: its tiles and kFewPieceCost
+};
+
+// Tiles of sequence b's keys, 0 when this kernel has no rows of it.
+struct FewSeq {
+  int qoff, T, S, tiles;
+};
+__device__ __forceinline__ FewSeq few_seq(const Params& p, int b) {
+  FewSeq q;
+  q.qoff = __ldg(p.cu_q + b);
+  q.T = __ldg(p.cu_q + b + 1) - q.qoff;
+  q.S = min(max(__ldg(p.seq_lens + b), 0), p.max_blocks * 16);
+  if (q.T <= 0 || q.T > p.tok_tile) q.T = 0;
+  q.tiles = q.T > 0 ? (q.S + kBN - 1) / kBN : 0;
+  return q;
+}
+
+// Length of the sequence on the line.
+__device__ __forceinline__ int few_extent(const FewParams& f, const FewSeq& q) {
+  return q.tiles == 0 ? 0 : f.seq_tiles > 0 ? f.seq_tiles : q.tiles + kFewPieceCost;
+}
+
+// The walk over a group's stretch of the line.
+struct FewWalk {
+  int b, lo;            // next piece: sequence b from its place lo on
+  long long pos, end;   // place on the line, end of the stretch
+  // the piece, of sequence pb
+  FewSeq q;
+  int pb;
+  int j0, n;            // first tile, tiles
+  bool whole, last;     // the whole sequence; its end
+  long long seq_pos;    // where the sequence begins
+
+  __device__ __forceinline__ bool next(const FewParams& f) {
+    for (; pos < end && b < f.p.B; ++b) {
+      q = few_seq(f.p, b);
+      const int extent = few_extent(f, q);
+      if (extent == 0) continue;
+      const int hi = static_cast<int>(min(static_cast<long long>(extent), lo + (end - pos)));
+      const int cost = f.seq_tiles > 0 ? 0 : kFewPieceCost;  // the first places hold no tile
+      j0 = max(lo - cost, 0);
+      n = max(min(hi - cost, q.tiles) - j0, 0);
+      whole = lo == 0 && hi == extent;
+      last = hi == extent;
+      seq_pos = pos - lo;
+      pos += hi - lo;
+      lo = 0;
+      pb = b++;
+      return true;
+    }
+    return false;
+  }
+};
+
 template <int R>
 constexpr size_t few_smem_bytes() { return sizeof(FewSmem<R>) + 1024; }
-
-// OR of `pred` over the 128 threads of the softmax warps (a barrier).
-__device__ __forceinline__ bool vote_or_128(bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(pred ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
 
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -96,386 +180,669 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   return r;
 }
 
-template <int COLS>
-__device__ __forceinline__ void tmem_load_cols(uint32_t taddr, uint32_t (&u)[COLS]) {
+// The sixteen values of every lane reduced over the warp: lane L returns the
+// result for value L / 2.  Each step halves the values that a lane keeps.
+template <bool kMax>
+__device__ __forceinline__ float warp_reduce16(const float2 (&x)[8], int lane) {
+  auto op = [](float a, float b) { return kMax ? fmaxf(a, b) : a + b; };
+  float v[16];
 #pragma unroll
-  for (int c = 0; c < COLS / 32; ++c) tmem_ld32_sync(taddr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&u[c * 32]));
+  for (int i = 0; i < 8; ++i) v[2 * i] = x[i].x, v[2 * i + 1] = x[i].y;
+#pragma unroll
+  for (int n = 8; n >= 1; n >>= 1) {
+    const bool high = lane & (2 * n);
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float keep = high ? v[i + n] : v[i], give = high ? v[i] : v[i + n];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, give, 2 * n));
+    }
+  }
+  return op(v[0], __shfl_xor_sync(0xffffffffu, v[0], 1));
 }
 
 template <int R>
-__global__ void __launch_bounds__(kFewThreads, kFewCtasPerSm)
+__global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
     prefill_fp8_few(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const __nv_bfloat16* __restrict__ q, const Params p) {
+                    const __nv_bfloat16* __restrict__ q, const __grid_constant__ FewParams f) {
   using C = FewConfig<R>;
+  const Params& p = f.p;
   extern __shared__ uint8_t smem_raw[];
   FewSmem<R>& sm = *reinterpret_cast<FewSmem<R>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  // blockIdx.x = (sequence, range, kv head), the kv head fastest
-  const int hk = static_cast<int>(blockIdx.x) % p.Hkv;
-  const int split = (static_cast<int>(blockIdx.x) / p.Hkv) % p.splits;
-  const int b = static_cast<int>(blockIdx.x) / p.Hkv / p.splits;
+  const int cta = blockIdx.x;
+  const int hk = cta % p.Hkv, group = cta / p.Hkv, groups = static_cast<int>(gridDim.x) / p.Hkv;
+  constexpr int kWarpCopy = C::kSoftmaxWarps, kWarpMma = C::kSoftmaxWarps + 1;
 
-  if (threadIdx.x == 128) {
+  if (warp == kWarpCopy && lane == 0) {
     for (int s = 0; s < C::kSlots; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
     }
-    mbar_init(&sm.q_ready, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.s_free[i], 4);
-      mbar_init(&sm.p_full[i], 4);
-      mbar_init(&sm.p_free[i], 1);
+      mbar_init(&sm.s_free[i], C::kSoftmaxWarps);
     }
+    for (int i = 0; i < kFewPieces; ++i) {
+      mbar_init(&sm.piece_full[i], 1);
+      mbar_init(&sm.piece_free[i], C::kSoftmaxWarps + 1);
+    }
+    mbar_init(&sm.p_full, C::kSoftmaxWarps);
+    mbar_init(&sm.p_free, 1);
     mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.o_free, C::kSoftmaxWarps);
+    mbar_init(&sm.mma_done, 1);
+    for (int i = 0; i < C::kWgs; ++i) {
+      mbar_init(&sm.vote[i], 4);
+      mbar_init(&sm.sync[i], 4);
+      sm.moved[i] = -1;
+    }
     sm.abort_flag = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
+  if (warp == kWarpMma) {
+    tmem_alloc(&sm.tmem_base, C::kTmem);
+    tmem_relinquish();
+  }
   grid_dependency_wait();
   grid_launch_dependents();
 
-  const int qoff = p.cu_q[b];
-  const int T = p.cu_q[b + 1] - qoff;
-  int S = p.seq_lens[b];
-  if (S < 0 || S > p.max_blocks * 16) {
-    if (threadIdx.x == 0 && hk == 0 && split == 0) atomicOr(&g_devstatus, kDevStatusBadSeqLen);
-    S = S < 0 ? 0 : p.max_blocks * 16;
-  }
-  if (T <= 0 || T > p.tok_tile) return;  // (tok_tile = R / G >= the largest T here)
-  const int rows = T * p.G;
-  const int j0 = split * p.chunk;
-  const int n = min(max((S + kBN - 1) / kBN - j0, 0), p.chunk);
-  if (n == 0) {
-    // no key in this range: the merge skips it, or there is none at all
-    for (int i = threadIdx.x; i < rows; i += kFewThreads) {
-      const size_t tok = static_cast<size_t>(qoff) + i / p.G;
-      const int head = hk * p.G + i % p.G;
-      if (tok >= static_cast<size_t>(p.total_q)) continue;
-      if (p.splits > 1) {
-        p.part_lse[(static_cast<size_t>(split) * p.total_q + tok) * p.Hq + head] = -INFINITY;
-      } else {
-        for (int e = 0; e < kD; e += 8) *reinterpret_cast<uint4*>(p.o + (tok * p.Hq + head) * kD + e) = make_uint4(0, 0, 0, 0);
-        if (p.lse != nullptr) p.lse[static_cast<size_t>(head) * p.total_q + tok] = -INFINITY;
+  // Length of the line and, with it, this group's stretch.  Sequences without a
+  // key are dealt out too: their rows become o = 0, lse = -inf.
+  if (warp == 0) {
+    long long total = 0;
+#pragma unroll 4
+    for (int b = lane; b < p.B; b += 32) {
+      const FewSeq s = few_seq(p, b);
+      const int raw = __ldg(p.seq_lens + b);
+      if (cta == 0 && (raw < 0 || raw > p.max_blocks * 16)) atomicOr(&g_devstatus, kDevStatusBadSeqLen);
+      total += few_extent(f, s);
+      if (s.tiles == 0 && b % gridDim.x == cta) {
+        f.meta[b] = make_int2(0, 0);
+        for (int t = 0; t < s.T && s.qoff + t < p.total_q; ++t)
+          for (int h = 0; h < p.Hq; ++h) {
+            const size_t tok = static_cast<size_t>(s.qoff) + t;
+            for (int e = 0; e < kD; e += 8)
+              *reinterpret_cast<uint4*>(p.o + (tok * p.Hq + h) * kD + e) = make_uint4(0u, 0u, 0u, 0u);
+            if (p.lse != nullptr) p.lse[static_cast<size_t>(h) * p.total_q + tok] = -INFINITY;
+          }
       }
     }
-    return;
-  }
-  if (warp == 5) {
-    tmem_alloc(&sm.tmem_base, C::kTmem);
-    tmem_relinquish();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    const long long even = (total + groups - 1) / groups;
+    const long long chunk = f.chunk > 0 ? f.chunk : even > kFewMinChunk ? even : kFewMinChunk;
+    const long long begin = chunk * group;
+    // the sequence that the stretch begins in
+    long long before = 0;
+    int b0 = p.B;
+    long long rest = 0;
+    for (int base = 0; base < p.B && b0 == p.B; base += 32) {
+      const int b = base + lane;
+      long long len = 0;
+      if (b < p.B) {
+        const FewSeq s = few_seq(p, b);
+        len = few_extent(f, s);
+      }
+      long long incl = len;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, begin < before + incl);
+      if (m != 0) {
+        const int w = __ffs(m) - 1;
+        b0 = base + w;
+        rest = begin - before - __shfl_sync(0xffffffffu, incl - len, w);  // places into sequence b0
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      sm.chunk = chunk;
+      sm.begin = begin;
+      sm.end = min(begin + chunk, total);
+      sm.b0 = b0;
+      sm.rest = rest;
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort_flag = &sm.abort_flag;
+  int jt = 0;  // tiles so far, over all pieces: rings and phases go by it
+  // The next piece, for the MMA warp's lane and the softmax warps.
+  auto take_piece = [&](int i, FewPiece& pc) -> bool {
+    if (!mbar_wait(&sm.piece_full[i % kFewPieces], (i / kFewPieces) & 1, abort_flag)) return false;
+    pc = sm.piece[i % kFewPieces];
+    return true;
+  };
 
-  if (warp == 4) {
+  if (warp == kWarpCopy) {
     // ------------------------------- copies -------------------------------
-    // Lane L < 8 issues the copy of block L of the tile.
+    // Also walks the line for the whole CTA and prepares each piece's q while
+    // the piece before is at work.  Lane L < 8 issues the copy of block L of
+    // the tile.
+    FewWalk walk;
+    walk.pos = sm.begin;
+    walk.end = sm.end;
+    walk.b = sm.b0;
+    walk.lo = static_cast<int>(sm.rest);
     int issued = 0;
     const uint64_t pol = l2_policy_evict_first();  // every byte is read once
     bool ok = true;
-    const int32_t* table = p.block_table + static_cast<size_t>(b) * p.max_blocks;
-    const int nblk_all = (S + 15) / 16;
-    int id_next = j0 * 8 + lane < nblk_all && lane < 8 ? __ldg(table + j0 * 8 + lane) : 0;
-    for (int j = 0; j < n && ok; ++j) {
-      const int blk0 = (j0 + j) * 8;
-      const int nblk = min(8, nblk_all - blk0);
-      const int id = id_next;
-      if (j + 1 < n) id_next = blk0 + 8 + lane < nblk_all && lane < 8 ? __ldg(table + blk0 + 8 + lane) : 0;
-      const bool in_pool = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
-      const uint32_t bad = __ballot_sync(0xffffffffu, lane < nblk && !in_pool);
-      if (bad && lane == 0) atomicOr(&g_devstatus, kDevStatusBadBlock);
-      const uint32_t bytes = static_cast<uint32_t>(nblk - __popc(bad)) * 16 * kD;
+    for (int i = 0; ok; ++i) {
+      const bool more = walk.next(f);
+      const int slot = i % kFewPieces;
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.piece_free[slot], ((i / kFewPieces) & 1) ^ 1, abort_flag));
+      if (!ok) break;
+      if (more && walk.n > 0) {
+        // q rows to e4m3 hi and lo terms: eight lanes a row, 16 elements each
+        constexpr int kBatch = 4;  // rows of four in flight
+        for (int r0 = 0; r0 < R; r0 += 4 * kBatch) {
+          uint32_t w[kBatch][8];
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int i = 2 * j + kv, s = i % C::kSlots;
-        if (lane == 0) {
-          ok = mbar_wait(&sm.empty[s], ((i / C::kSlots) & 1) ^ 1, abort_flag);
-          if (ok) mbar_arrive_expect_tx(&sm.full[s], bytes);
+          for (int t = 0; t < kBatch; ++t) {
+            const int r = r0 + 4 * t + (lane >> 3), u = lane & 7;
+            const int tok = walk.q.qoff + r / p.G;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[t][e] = 0;
+            if (r < walk.q.T * p.G && tok < p.total_q) {
+              const uint4* src = reinterpret_cast<const uint4*>(
+                  q + (static_cast<size_t>(tok) * p.Hq + hk * p.G + r % p.G) * kD + u * 16);
+              const uint4 a = __ldg(src), c = __ldg(src + 1);
+              w[t][0] = a.x, w[t][1] = a.y, w[t][2] = a.z, w[t][3] = a.w;
+              w[t][4] = c.x, w[t][5] = c.y, w[t][6] = c.z, w[t][7] = c.w;
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < kBatch; ++t) {
+            const int r = r0 + 4 * t + (lane >> 3), u = lane & 7;
+            uint32_t top = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = __vmaxu2(top, w[t][e] & 0x7fff7fffu);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const RowScale rs = row_scale(max(top & 0xffffu, top >> 16));
+            uint4 hi, lo;
+            split_e4m3(w[t], rs.up, hi, lo);
+            *reinterpret_cast<uint4*>(sm.q[slot] + r * 128 + ((u ^ (r & 7)) << 4)) = hi;
+            *reinterpret_cast<uint4*>(sm.q[slot] + (R + r) * 128 + ((u ^ (r & 7)) << 4)) = lo;
+            if (u == 0) {
+              sm.sl2[slot][r] = row_score_scale(p.scale_log2, rs);
+              sm.lim[slot][r] = r >= walk.q.T * p.G ? 0x7fffffff
+                                : p.causal          ? walk.q.S - walk.q.T + r / p.G
+                                                    : walk.q.S - 1;
+            }
+          }
         }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-        if (lane < nblk && in_pool)
-          tma_load_2d_hint(sm.ring[s] + lane * 16 * 128, kv ? &tmV : &tmK, &sm.full[s], hk * kD, id * 16, pol);
-        issued = i + 1;
+        fence_proxy_async_smem();
+      }
+      if (lane == 0) {
+        FewPiece& pc = sm.piece[slot];
+        pc.b = more ? walk.pb : -1;
+        pc.j0 = walk.j0;
+        pc.n = walk.n;
+        pc.qoff = walk.q.qoff;
+        pc.T = walk.q.T;
+        pc.S = walk.q.S;
+        pc.whole = walk.whole;
+        pc.last = walk.last;
+        pc.g0 = more ? static_cast<int>(walk.seq_pos / sm.chunk) : 0;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.piece_full[slot]);
+      if (!more) break;
+      const int32_t* table = p.block_table + static_cast<size_t>(walk.pb) * p.max_blocks;
+      const int nblk_all = (walk.q.S + 15) / 16;
+      int id_next = lane < 8 && walk.n > 0 && walk.j0 * 8 + lane < nblk_all ? __ldg(table + walk.j0 * 8 + lane) : 0;
+      for (int j = 0; j < walk.n && ok; ++j, ++jt) {
+        const int blk0 = (walk.j0 + j) * 8;
+        const int nblk = min(8, nblk_all - blk0);
+        const int id = id_next;
+        if (j + 1 < walk.n) id_next = lane < 8 && blk0 + 8 + lane < nblk_all ? __ldg(table + blk0 + 8 + lane) : 0;
+        const bool in_pool = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
+        const uint32_t bad = __ballot_sync(0xffffffffu, lane < nblk && !in_pool);
+        if (bad && lane == 0) atomicOr(&g_devstatus, kDevStatusBadBlock);
+        const uint32_t bytes = static_cast<uint32_t>(nblk - __popc(bad)) * 16 * kD;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int t = 2 * jt + kv, s = t % C::kSlots;
+          if (lane == 0) {
+            ok = mbar_wait(&sm.empty[s], ((t / C::kSlots) & 1) ^ 1, abort_flag);
+            if (ok) {
+              if (kv == 0) sm.bad[jt % kFewBad] = bad;
+              mbar_arrive_expect_tx(&sm.full[s], bytes);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          if (lane < nblk && in_pool)
+            tma_load_2d_hint(sm.ring[s] + lane * 16 * 128, kv ? &tmV : &tmK, &sm.full[s], hk * kD, id * 16, pol);
+          issued = t + 1;
+        }
       }
     }
     if (lane == 0 && *abort_flag)  // let the copies already issued land before shared memory is released
       for (int i = max(0, issued - C::kSlots); i < issued; ++i)
         mbar_wait_drain(&sm.full[i % C::kSlots], (i / C::kSlots) & 1);
-  } else if (warp == 5) {
+  } else if (warp == kWarpMma) {
     // ----------------------------- MMA issuer -----------------------------
     if (lane == 0) {
       constexpr uint32_t idesc_qk = make_idesc_fmt0(128, C::kN, 0, 0);  // K, (Q_hi ; Q_lo): head dim contiguous
       // V (e4m3), P (e5m2: format 1 of B), both with the keys apart
       constexpr uint32_t idesc_pv = make_idesc_fmt0(128, C::kNP, 1, 1) | 1u << 10;
-      bool ok = mbar_wait(&sm.q_ready, 0, abort_flag);
-      tc_fence_after();
-      const uint32_t qbase = smem_u32(sm.q);
-      auto issue_qk = [&](int j) -> bool {
-        const int i = 2 * j, s = i % C::kSlots, buf = j & 1;
-        if (!mbar_wait(&sm.full[s], (i / C::kSlots) & 1, abort_flag)) return false;
-        if (!mbar_wait(&sm.s_free[buf], ((j >> 1) & 1) ^ 1, abort_flag)) return false;
+      const uint32_t pbase = smem_u32(sm.p);
+      bool ok = true;
+      for (int i = 0, piece = 0; ok; ++i) {
+        FewPiece pc;
+        if (!(ok = take_piece(i, pc))) break;
+        if (pc.n == 0 || pc.b < 0) mbar_arrive(&sm.piece_free[i % kFewPieces]);
+        if (pc.b < 0) break;
+        if (pc.n == 0) continue;
+        const uint32_t qbase = smem_u32(sm.q[i % kFewPieces]);
+        // O^T of the piece before read
+        if (!(ok = mbar_wait(&sm.o_free, (piece & 1) ^ 1, abort_flag))) break;
         tc_fence_after();
-        const uint32_t kbase = smem_u32(sm.ring[s]);
+        // Whichever product is ready goes: O^T of tile tp (it frees a V tile and
+        // P), S^T of tile ts (up to two ahead).
+        const int t0 = jt, t1 = jt + pc.n;
+        int ts = t0, tp = t0;
+        uint64_t since = 0;  // when it last had to wait
+        uint32_t idle = 0;
+        while (tp < t1) {
+          bool done = false;
+          if (tp < ts) {
+            const int t = 2 * tp + 1, s = t % C::kSlots;
+            if (mbar_test(&sm.p_full, tp & 1) && mbar_test(&sm.full[s], (t / C::kSlots) & 1)) {
+              tc_fence_after();
+              const uint32_t vbase = smem_u32(sm.ring[s]);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          umma_ss_f8(tmem + buf * C::kN, make_sdesc_sw128(kbase + kk * 32, 16, 1024),
-                     make_sdesc_sw128(qbase + kk * 32, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
-        umma_commit(&sm.s_full[buf]);
-        umma_commit(&sm.empty[s]);
-        return true;
-      };
-      if (ok) ok = issue_qk(0);
-      for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n && !(ok = issue_qk(j + 1))) break;
-        const int i = 2 * j + 1, s = i % C::kSlots, buf = j & 1;
-        if (!(ok = mbar_wait(&sm.full[s], (i / C::kSlots) & 1, abort_flag))) break;
-        if (!(ok = mbar_wait(&sm.p_full[buf], (j >> 1) & 1, abort_flag))) break;
-        tc_fence_after();
-        const uint32_t vbase = smem_u32(sm.ring[s]), pbase = smem_u32(sm.p[buf]);
+              for (int kk = 0; kk < 4; ++kk)  // 32 keys at a time
+                umma_ss_f8(tmem + 2 * C::kN, make_sdesc_sw128(vbase + kk * 32 * 128, 16, 1024),
+                           make_sdesc(pbase + kk * 32 * C::kNP, 16, 8 * C::kNP, C::kPLayout), idesc_pv,
+                           (tp > t0 || kk > 0) ? 1u : 0u);
+              umma_commit(&sm.p_free);
+              umma_commit(&sm.empty[s]);
+              ++tp;
+              done = true;
+            }
+          }
+          if (ts < t1 && ts < tp + 2) {
+            const int t = 2 * ts, s = t % C::kSlots, buf = ts & 1;
+            if (mbar_test(&sm.full[s], (t / C::kSlots) & 1) && mbar_test(&sm.s_free[buf], ((ts >> 1) & 1) ^ 1)) {
+              tc_fence_after();
+              const uint32_t kbase = smem_u32(sm.ring[s]);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)  // 32 keys at a time
-          umma_ss_f8(tmem + 2 * C::kN, make_sdesc_sw128(vbase + kk * 32 * 128, 16, 1024),
-                     make_sdesc(pbase + kk * 32 * C::kNP, 16, 8 * C::kNP, C::kPLayout), idesc_pv,
-                     (j > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&sm.p_free[buf]);
-        umma_commit(&sm.empty[s]);
+              for (int kk = 0; kk < 4; ++kk)
+                umma_ss_f8(tmem + buf * C::kN, make_sdesc_sw128(kbase + kk * 32, 16, 1024),
+                           make_sdesc_sw128(qbase + kk * 32, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
+              umma_commit(&sm.s_full[buf]);
+              umma_commit(&sm.empty[s]);
+              if (ts == t1 - 1) umma_commit(&sm.piece_free[i % kFewPieces]);  // q has been read
+              ++ts;
+              done = true;
+            }
+          }
+          if (done) {
+            idle = 0;
+          } else if ((++idle & 63u) == 0) {  // the limit of mbar_wait
+            const uint64_t now = globaltimer_ns();
+            if (idle == 64) since = now;
+            if (*abort_flag || now - since > kWaitLimitNs) {
+              if (!*abort_flag) atomicOr(&g_devstatus, kDevStatusTimeout);
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
+          }
+        }
+        jt = t1;
+        if (ok) umma_commit(&sm.o_full);
+        ++piece;
       }
       // complete once every MMA issued above is, also after an abort
-      umma_commit(&sm.o_full);
-      mbar_wait_drain(&sm.o_full, 0);
+      umma_commit(&sm.mma_done);
+      mbar_wait_drain(&sm.mma_done, 0);
     }
   } else {
     // ------------------------------- softmax -------------------------------
-    const int k = threadIdx.x;  // key of the tile, lane of S^T; d of O^T
-    // q rows to e4m3 hi and lo terms: eight lanes a row, 16 elements each
-    for (int r0 = 0; r0 < R; r0 += 16) {
-      const int r = r0 + (k >> 3), u = k & 7;
-      const int tok = r / p.G;
-      const bool real = r < rows && static_cast<size_t>(qoff) + tok < static_cast<size_t>(p.total_q);
-      uint32_t w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 0;
-      if (real) {
-        const uint4* src = reinterpret_cast<const uint4*>(
-            q + ((static_cast<size_t>(qoff) + tok) * p.Hq + hk * p.G + r - tok * p.G) * kD + u * 16);
-        const uint4 a = __ldg(src), c = __ldg(src + 1);
-        w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = c.x, w[5] = c.y, w[6] = c.z, w[7] = c.w;
-      }
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const RowScale rs = row_scale(max(top & 0xffffu, top >> 16));
-      uint4 hi, lo;
-      split_e4m3(w, rs.up, hi, lo);
-      *reinterpret_cast<uint4*>(sm.q + r * 128 + ((u ^ (r & 7)) << 4)) = hi;
-      *reinterpret_cast<uint4*>(sm.q + (R + r) * 128 + ((u ^ (r & 7)) << 4)) = lo;
-      if (u == 0) {
-        sm.sl2[r] = row_score_scale(p.scale_log2, rs);
-        sm.off[r] = kFewUnseen;
-        sm.lim[r] = r >= rows ? 0x7fffffff : p.causal ? S - T + tok : S - 1;
-      }
-    }
-    fence_proxy_async_smem();
-    named_barrier_sync(2, 128);
-    if (lane == 0) mbar_arrive(&sm.q_ready);
-
-    float l[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) l[r] = 0.f;
-    const uint32_t lane_off = uint32_t(warp * 32) << 16;
-    const uint32_t tO = tmem + lane_off + 2 * C::kN;
-    const int32_t* table = p.block_table + static_cast<size_t>(b) * p.max_blocks;
-    const int first_lim = p.causal ? S - T : S - 1;  // last key that every row sees
+    const int k = threadIdx.x & 127;  // key of the tile, lane of S^T; d of O^T
+    const int wg = warp >> 2, h0 = wg * 16;  // this warpgroup's 16 rows
+    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t tO = tmem + lane_off + 2 * C::kN + h0;  // term t: t * R columns on
+    float* const off = sm.off[warp];
+    float* const alpha = sm.alpha[warp];
     // After a wait that gave up a warp goes on without waiting (the output is
-    // then undefined): the barriers below count on all four warps.
+    // then undefined and not written).
     bool ok = true;
-    int id_next = (j0 * 8 + (k >> 4)) * 16 < S ? __ldg(table + j0 * 8 + (k >> 4)) : -1;
-    for (int j = 0; j < n; ++j) {
-      const int buf = j & 1;
-      const int pos = (j0 + j) * kBN + k;
-      const bool dead = pos >= S || static_cast<unsigned>(id_next) >= static_cast<unsigned>(p.num_blocks);
-      if (j + 1 < n) id_next = (pos & ~15) + kBN < S ? __ldg(table + (j0 + j + 1) * 8 + (k >> 4)) : -1;
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[buf], (j >> 1) & 1, abort_flag));
-      tc_fence_after();
-      float x[R];
-      {
-        uint32_t s[C::kN];
-        tmem_load_cols<C::kN>(tmem + lane_off + buf * C::kN, s);
-#pragma unroll
-        for (int r = 0; r < R; ++r) x[r] = __uint_as_float(s[r]) + __uint_as_float(s[R + r]);
-      }
-      tc_fence_before();
+    int syncs = 0, votes = 0;
+    auto sync_wg = [&]() {  // the warpgroup's four warps, with a bounded wait
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.s_free[buf]);
-      if (__any_sync(0xffffffffu, dead || pos > first_lim)) {
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          if (dead || pos > sm.lim[r]) x[r] = -INFINITY;
+      if (lane == 0) mbar_arrive(&sm.sync[wg]);
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.sync[wg], syncs & 1, abort_flag));
+      ++syncs;
+    };
+    for (int i = 0, piece = 0; ok; ++i) {
+      FewPiece pc;
+      ok = __all_sync(0xffffffffu, take_piece(i, pc));
+      if (!ok || pc.b < 0) break;
+      const int T = pc.T, S = pc.S, qoff = pc.qoff, n = pc.n;
+      const int rows = T * p.G;
+      const bool whole = pc.whole != 0;
+      const int slot = 2 * cta + (pc.last ? 0 : 1);  // of a cut sequence's piece
+      if (pc.last && hk == 0 && threadIdx.x == 0) f.meta[pc.b] = make_int2(pc.g0, group);
+      if (n == 0) {  // nothing on this piece: the merge skips it
+        if (threadIdx.x < rows) f.part_lse[static_cast<size_t>(slot) * R + threadIdx.x] = -INFINITY;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.piece_free[i % kFewPieces]);
+        continue;
       }
-      // exponents x * sl2 + off, and whether one of them moves its row's reference
-      float y[R];
-      bool over = false;
-#pragma unroll
-      for (int r = 0; r < R; r += 4) {
-        const float4 sc = *reinterpret_cast<const float4*>(&sm.sl2[r]);
-        const float4 of = *reinterpret_cast<const float4*>(&sm.off[r]);
-        y[r] = fmaf(x[r], sc.x, of.x);
-        y[r + 1] = fmaf(x[r + 1], sc.y, of.y);
-        y[r + 2] = fmaf(x[r + 2], sc.z, of.z);
-        y[r + 3] = fmaf(x[r + 3], sc.w, of.w);
-        over |= fmaxf(fmaxf(y[r], y[r + 1]), fmaxf(y[r + 2], y[r + 3])) > kFewLimit;
-      }
-      if (vote_or_128(over)) {
-        // new references: the maxima over the tile's keys
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          float m = x[r] * sm.sl2[r];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          if (lane == 0) sm.red[warp][r] = m;
-        }
-        named_barrier_sync(2, 128);
-        if (k < R) {
-          const float m = fmaxf(fmaxf(sm.red[0][k], sm.red[1][k]), fmaxf(sm.red[2][k], sm.red[3][k]));
-          const float old = sm.off[k];
-          const bool move = m + old > kFewLimit;
-          const float off = move ? kFewShift - m : old;
-          sm.alpha[k] = move ? ex2_approx(off - old) : 1.f;
-          sm.off[k] = off;
-        }
-        named_barrier_sync(2, 128);
-        if (j > 0) {
-          // O^T holds the tiles before: all their MMAs first, then one factor a column
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free[buf ^ 1], ((j - 1) >> 1) & 1, abort_flag));
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < C::kNP / 32; ++c) {
-            uint32_t u[32];
-            tmem_ld32_sync(tO + c * 32, u);
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              u[i] = __float_as_uint(__uint_as_float(u[i]) * sm.alpha[(c * 32 + i) & (R - 1)]);
-            tmem_st_x32(tO + c * 32, u);
-          }
-          tmem_st_wait();
-        }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          l[r] *= sm.alpha[r];
-          y[r] = fmaf(x[r], sm.sl2[r], sm.off[r]);
-        }
-      }
-      uint32_t pt[4][R / 4];  // the weights' e5m2 terms, four rows to a word
-#pragma unroll
-      for (int r = 0; r < R; r += 4) {
-        const float p0 = ex2_approx(y[r]), p1 = ex2_approx(y[r + 1]), p2 = ex2_approx(y[r + 2]),
-                    p3 = ex2_approx(y[r + 3]);
-        l[r] += p0;
-        l[r + 1] += p1;
-        l[r + 2] += p2;
-        l[r + 3] += p3;
-        uint32_t a = pack_f16x2(p0, p1), c = pack_f16x2(p2, p3);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          pt[t][r / 4] = prmt(a, c, 0x7531);  // the four top bytes
-          if (t < 3) {
-            a = hsub2(a, a & 0xff00ff00u);
-            c = hsub2(c, c & 0xff00ff00u);
-          }
-        }
-      }
-      if (ok && j >= 2)  // the P buffer's last reader: the tile two before
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free[buf], ((j - 2) >> 1) & 1, abort_flag));
-      const int sw = C::kNP == 64 ? (k >> 1) & 3 : k & 7;
-      uint8_t* prow = sm.p[buf] + k * C::kNP;
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int u = 0; u < R / 16; ++u)
-          *reinterpret_cast<uint4*>(prow + (((t * (R / 16) + u) ^ sw) << 4)) =
-              make_uint4(pt[t][4 * u], pt[t][4 * u + 1], pt[t][4 * u + 2], pt[t][4 * u + 3]);
-      if (__any_sync(0xffffffffu, dead)) {
-        // no weight falls on this key, but its V row may hold anything (NaN codes): cleared before the MMA reads it
-        const int i = 2 * j + 1;
-        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[i % C::kSlots], (i / C::kSlots) & 1, abort_flag));
-        if (dead && ok)
-#pragma unroll
-          for (int u = 0; u < 8; ++u)
-            *reinterpret_cast<uint4*>(sm.ring[i % C::kSlots] + k * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_proxy_async_smem();
-      tc_fence_before();
+      const float* const sl2 = sm.sl2[i % kFewPieces] + h0;
+      const int* const lim = sm.lim[i % kFewPieces] + h0;
+      if (lane < 16) off[lane] = kFewUnseen;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[buf]);
-    }
 
-    // Row sums over the 128 keys, then O^T / l.
-    named_barrier_sync(2, 128);  // sm.red, sm.off: every warp is past its last use
+      float2 l[8];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float v = l[r];
+      for (int e = 0; e < 8; ++e) l[e] = make_float2(0.f, 0.f);
+      const int first_lim = p.causal ? S - T : S - 1;  // last key that every row sees
+      int pos = pc.j0 * kBN + k;                         // this thread's key
+      for (int j = 0; j < n; ++j, ++jt, pos += kBN) {
+        const int buf = jt & 1;
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[buf], (jt >> 1) & 1, abort_flag));
+        tc_fence_after();
+        const bool dead = pos >= S || ((sm.bad[jt % kFewBad] >> (k >> 4)) & 1u);
+        const bool masked = __any_sync(0xffffffffu, dead || pos > first_lim);
+        float2 w[8];        // scores, exponents, weights
+        uint32_t pt[4][4];  // the weights' e5m2 terms, four rows to a word
+        // The first tile sets the references; a later one is done again in the
+        // rare case that one of its scores moves a reference.
+        for (bool update = j == 0;; update = true) {
+          {
+            uint32_t hi[16], lo[16];
+            tmem_ld16x2_sync(tmem + lane_off + buf * C::kN + h0, hi, tmem + lane_off + buf * C::kN + R + h0, lo);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0) sm.red[warp][r] = v;
-    }
-    named_barrier_sync(2, 128);
-    if (k < rows) {
-      const float v = (sm.red[0][k] + sm.red[1][k]) + (sm.red[2][k] + sm.red[3][k]);
-      sm.alpha[k] = v == 0.f ? 0.f : p.v_scale / v;
-      const float lse = v == 0.f ? -INFINITY : (log2f(v) - sm.off[k]) * 0.69314718055994531f;
-      const size_t tok = static_cast<size_t>(qoff) + k / p.G;
-      const int head = hk * p.G + k % p.G;
-      if (ok && tok < static_cast<size_t>(p.total_q)) {
-        if (p.splits > 1)
-          p.part_lse[(static_cast<size_t>(split) * p.total_q + tok) * p.Hq + head] = lse;
-        else if (p.lse != nullptr)
-          p.lse[static_cast<size_t>(head) * p.total_q + tok] = lse;
+            for (int i = 0; i < 8; ++i)
+              w[i] = __fadd2_rn(make_float2(__uint_as_float(hi[2 * i]), __uint_as_float(hi[2 * i + 1])),
+                                make_float2(__uint_as_float(lo[2 * i]), __uint_as_float(lo[2 * i + 1])));
+          }
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (dead || pos > lim[2 * i]) w[i].x = -INFINITY;
+              if (dead || pos > lim[2 * i + 1]) w[i].y = -INFINITY;
+            }
+          }
+          if (update) {
+            // new references: the maxima over the tile's keys
+            float2 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = make_float2(w[i].x * sl2[2 * i], w[i].y * sl2[2 * i + 1]);
+            const float m = warp_reduce16<true>(x, lane);
+            if (!(lane & 1)) sm.top[warp][lane >> 1] = m;
+            sync_wg();
+            if (lane < 16) {
+              const float* t = &sm.top[wg * 4][lane];
+              const float m4 = fmaxf(fmaxf(t[0], t[16]), fmaxf(t[32], t[48]));
+              const float old = off[lane];
+              const bool move = m4 + old > kFewLimit;
+              alpha[lane] = move ? ex2_approx(kFewShift - m4 - old) : 1.f;
+              off[lane] = move ? kFewShift - m4 : old;
+            }
+            __syncwarp();
+            if (j > 0) {
+              // O^T holds the tiles before: all their MMAs first, then one factor a column
+              if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free, (jt - 1) & 1, abort_flag));
+              tc_fence_after();
+#pragma unroll
+              for (int t = 0; t < 4; ++t) {
+                uint32_t u[16];
+                tmem_ld16_sync(tO + t * R, u);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha[i]);
+                tmem_st_x16(tO + t * R, u);
+              }
+              tmem_st_wait();
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              l[i].x *= alpha[2 * i];
+              l[i].y *= alpha[2 * i + 1];
+            }
+          }
+          // exponents, and whether one of them moves its row's reference; the
+          // answer is awaited only after the exponentials
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const float4 sc = *reinterpret_cast<const float4*>(&sl2[2 * i]);
+            const float4 of = *reinterpret_cast<const float4*>(&off[2 * i]);
+            w[i] = __ffma2_rn(w[i], make_float2(sc.x, sc.y), make_float2(of.x, of.y));
+            w[i + 1] = __ffma2_rn(w[i + 1], make_float2(sc.z, sc.w), make_float2(of.z, of.w));
+            top = fmax3(fmax3(top, w[i].x, w[i].y), w[i + 1].x, w[i + 1].y);
+          }
+          if (!update) {
+            if (top > kFewLimit) *static_cast<volatile int*>(&sm.moved[wg]) = jt;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.vote[wg]);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float2 &p0 = w[2 * i], &p1 = w[2 * i + 1];
+            p0 = make_float2(ex2_approx(p0.x), ex2_approx(p0.y));
+            p1 = make_float2(ex2_approx(p1.x), ex2_approx(p1.y));
+            uint32_t a = pack_f16x2(p0.x, p0.y), c = pack_f16x2(p1.x, p1.y);
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              pt[t][i] = prmt(a, c, 0x7531);  // the four top bytes
+              if (t < 3) {
+                a = hsub2(a, a & 0xff00ff00u);
+                c = hsub2(c, c & 0xff00ff00u);
+              }
+            }
+          }
+          if (update) break;
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.vote[wg], votes & 1, abort_flag));
+          ++votes;
+          if (!ok || *static_cast<volatile int*>(&sm.moved[wg]) != jt) break;
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.s_free[buf]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) l[i] = __fadd2_rn(l[i], w[i]);
+        // the P buffer's last readers: the tile before; the piece before, which
+        // staged its output there
+        if (ok && jt >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free, (jt - 1) & 1, abort_flag));
+        if (ok && j == 0 && piece > 0)
+          ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_free, (piece - 1) & 1, abort_flag));
+        const int sw = C::kNP == 64 ? (k >> 1) & 3 : k & 7;
+        uint8_t* prow = sm.p + k * C::kNP;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          *reinterpret_cast<uint4*>(prow + (((t * (R / 16) + h0 / 16) ^ sw) << 4)) =
+              make_uint4(pt[t][0], pt[t][1], pt[t][2], pt[t][3]);
+        if (wg == 0 && __any_sync(0xffffffffu, dead)) {
+          // no weight falls on this key, but its V row may hold anything (NaN codes): cleared before the MMA reads it
+          const int t = 2 * jt + 1;
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[t % C::kSlots], (t / C::kSlots) & 1, abort_flag));
+          if (dead && ok)
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              *reinterpret_cast<uint4*>(sm.ring[t % C::kSlots] + k * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full);
       }
-    }
-    named_barrier_sync(2, 128);
-    if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_full, 0, abort_flag));
-    if (ok) {
-      tc_fence_after();
-      float sum[R];  // the four terms' products
+
+      // Row sums over the 128 keys, then O^T / l.
       {
-        uint32_t u[2 * R], v[2 * R];
-        tmem_load_cols<2 * R>(tO, u);
-        tmem_load_cols<2 * R>(tO + 2 * R, v);
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-          sum[r] = (__uint_as_float(u[r]) + __uint_as_float(u[R + r])) +
-                   (__uint_as_float(v[r]) + __uint_as_float(v[R + r]));
+        const float v = warp_reduce16<false>(l, lane);
+        if (!(lane & 1)) sm.sum[warp][lane >> 1] = v;
       }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const size_t tok = static_cast<size_t>(qoff) + r / p.G;
-        if (r < rows && tok < static_cast<size_t>(p.total_q)) {
-          const float o = sum[r] * sm.alpha[r];
-          const size_t row = tok * p.Hq + hk * p.G + r % p.G;
-          if (p.splits > 1)
-            p.part_o[(static_cast<size_t>(split) * p.total_q * p.Hq + row) * kD + k] = o;
-          else
-            p.o[row * kD + k] = __float2bfloat16_rn(o);
+      sync_wg();
+      if (lane < 16) {
+        const float* t = &sm.sum[wg * 4][lane];
+        const float v = (t[0] + t[16]) + (t[32] + t[48]);
+        alpha[lane] = v == 0.f ? 0.f : p.v_scale / v;
+        const int r = h0 + lane;
+        if ((warp & 3) == 0 && r < rows && ok) {
+          const float lse = v == 0.f ? -INFINITY : (log2f(v) - off[lane]) * 0.69314718055994531f;
+          const int tok = qoff + r / p.G;
+          if (!whole)
+            f.part_lse[static_cast<size_t>(slot) * R + r] = lse;
+          else if (p.lse != nullptr && tok < p.total_q)
+            p.lse[static_cast<size_t>(hk * p.G + r % p.G) * p.total_q + tok] = lse;
         }
       }
+      __syncwarp();
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_full, piece & 1, abort_flag));
+      tc_fence_after();
+      float sum[16];  // the four terms' products
+      {
+        uint32_t u[16], v[16];
+        tmem_ld16x2_sync(tO, u, tO + R, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum[e] = __uint_as_float(u[e]) + __uint_as_float(v[e]);
+        tmem_ld16x2_sync(tO + 2 * R, u, tO + 3 * R, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum[e] = (sum[e] + (__uint_as_float(u[e]) + __uint_as_float(v[e]))) * alpha[e];
+      }
+      if (!whole) {
+        float* dst = f.part_o + (static_cast<size_t>(slot) * R + h0) * kD + k;
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (ok && h0 + e < rows) dst[e * kD] = sum[e];
+      } else {
+        // through the P buffer (its last reader is done) to whole rows
+        __nv_bfloat16* stage = reinterpret_cast<__nv_bfloat16*>(sm.p + wg * 16 * kD * 2);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) stage[e * kD + k] = __float2bfloat16_rn(sum[e]);
+        sync_wg();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = e * 8 + (k >> 4);
+          const int tok = qoff + (h0 + r) / p.G;
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + r * kD + (k & 15) * 8);
+          if (ok && h0 + r < rows && tok < p.total_q)
+            *reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(tok) * p.Hq + hk * p.G + (h0 + r) % p.G) * kD +
+                                      (k & 15) * 8) = x;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.o_free);  // O^T and the staged rows have been read
+        mbar_arrive(&sm.piece_free[i % kFewPieces]);
+      }
+      ++piece;
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) {
+  if (warp == kWarpMma) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmem);
   }
+}
+
+// Merge of the pieces of cut sequences; a kv head's pieces lie at slots 2 c + 1
+// of its CTA c in each of the sequence's groups but the last, whose piece lies at
+// 2 c.  Weights 2^(lse_i - M), fixed order.  CTA = four warps: a row each (many
+// sequences), or (few sequences, each in many pieces) all four on one row, pieces
+// w, w + 4, ..
+template <int R, int ROWS>
+__global__ void __launch_bounds__(128) prefill_fp8_few_merge(const __grid_constant__ FewParams f) {
+  static_assert(ROWS == 1 || ROWS == 4, "rows of a CTA");
+  const Params& p = f.p;
+  constexpr int kStep = 4 / ROWS;  // warps on a row
+  constexpr float kLog2e = 1.4426950408889634f;
+  __shared__ float4 s_acc[4][32];
+  __shared__ float s_m[4], s_w[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * ROWS + (ROWS == 4 ? warp : 0);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int b = blockIdx.x / p.Hkv, hk = blockIdx.x % p.Hkv;
+  const int2 m = f.meta[b];
+  if (m.x == m.y) return;  // finished on one stretch
+  const FewSeq q = few_seq(p, b);
+  const int tok = q.qoff + r / p.G;
+  if (r >= q.T * p.G || tok >= p.total_q) return;  // (the whole CTA when it has one row)
+  const int head = hk * p.G + r % p.G;
+  const int pieces = m.y - m.x + 1;
+  auto slot_row = [&](int i) {
+    return (2 * (static_cast<size_t>(m.x + i) * p.Hkv + hk) + (i + 1 < pieces ? 1 : 0)) * R + r;
+  };
+  float M = -INFINITY, w = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kUnroll = 8;
+  for (int i0 = kStep > 1 ? warp : 0; i0 < pieces; i0 += kUnroll * kStep) {
+    float lv[kUnroll];
+    float4 v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kStep;
+      const size_t at = slot_row(min(i, pieces - 1));
+      lv[u] = i < pieces ? f.part_lse[at] * kLog2e : -INFINITY;
+      v[u] = *reinterpret_cast<const float4*>(f.part_o + at * kD + lane * 4);
+    }
+    float top = M;
+    bool any = false;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      top = fmaxf(top, lv[u]);
+      any |= lv[u] != -INFINITY;  // a NaN counts
+    }
+    if (!any) continue;
+    const float keep = M == -INFINITY ? 0.f : ex2_approx(M - top);
+    M = top;
+    w *= keep;
+    acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (lv[u] == -INFINITY) continue;  // an empty piece has no o
+      const float wk = ex2_approx(lv[u] - M);
+      w += wk;
+      acc.x = fmaf(wk, v[u].x, acc.x);
+      acc.y = fmaf(wk, v[u].y, acc.y);
+      acc.z = fmaf(wk, v[u].z, acc.z);
+      acc.w = fmaf(wk, v[u].w, acc.w);
+    }
+  }
+  if constexpr (ROWS == 1) {
+    s_acc[warp][lane] = acc;
+    if (lane == 0) s_m[warp] = M, s_w[warp] = w;
+    __syncthreads();
+    if (warp > 0) return;
+    M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    w = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (s_w[i] == 0.f) continue;  // (a NaN sum is kept)
+      const float wk = ex2_approx(s_m[i] - M);
+      const float4 x = s_acc[i][lane];
+      w = fmaf(wk, s_w[i], w);
+      acc.x = fmaf(wk, x.x, acc.x);
+      acc.y = fmaf(wk, x.y, acc.y);
+      acc.z = fmaf(wk, x.z, acc.z);
+      acc.w = fmaf(wk, x.w, acc.w);
+    }
+  }
+  const float inv = w == 0.f ? 0.f : 1.f / w;
+  *reinterpret_cast<uint2*>(p.o + (static_cast<size_t>(tok) * p.Hq + head) * kD + lane * 4) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  if (p.lse != nullptr && lane == 0)
+    p.lse[static_cast<size_t>(head) * p.total_q + tok] =
+        w == 0.f ? -INFINITY : (M + log2f(w)) * 0.69314718055994531f;
 }
 
 }  // namespace prefill8
