@@ -1082,14 +1082,15 @@ int launch_prefill_fp8_few(const CUtensorMap& mk, const CUtensorMap& mv, const v
     if (groups > most) groups = most;
   }
   const long long grid = groups * p.Hkv;
-  if (grid > 0x3fffffffLL || units > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
+  const long long line = static_cast<long long>(p.B) * ((f.seq_tiles ? f.seq_tiles : max_tiles) + prefill8::kFewPieceCost);
+  if (grid > 0x3fffffffLL || units > 0x7fffffffLL || line > 0x7ff00000LL) return ATTN_ERR_UNSUPPORTED;
   const size_t slots = static_cast<size_t>(grid) * 2;
   void* ws = nullptr;
-  if (int rc = workspace(&ws, slots * R * (prefill8::kD + 1) * sizeof(float) + p.B * sizeof(int2), stream, st))
+  if (int rc = workspace(&ws, slots * R * (prefill8::kD + 1) * sizeof(float) + p.B * sizeof(int4), stream, st))
     return rc;
   f.part_o = static_cast<float*>(ws);
   f.part_lse = f.part_o + slots * R * prefill8::kD;
-  f.meta = reinterpret_cast<int2*>(f.part_lse + slots * R);
+  f.meta = reinterpret_cast<int4*>(f.part_lse + slots * R);
   int rc = launch_pdl(prefill8::prefill_fp8_few<R>, dim3(static_cast<unsigned>(grid)), dim3(prefill8::FewConfig<R>::kThreads),
                       prefill8::few_smem_bytes<R>(), stream, mk, mv, static_cast<const __nv_bfloat16*>(q), f);
   if (rc == ATTN_OK && num_splits != 1) {

@@ -46,6 +46,8 @@
 // joins them.
 #pragma once
 
+#include <climits>
+
 #include "prefill_fp8_sm100.cuh"
 
 namespace attn {
@@ -93,7 +95,7 @@ struct __align__(1024) FewSmem {
   uint8_t p[C::kPBytes];
   FewPiece piece[kFewPieces];
   alignas(16) float sl2[kFewPieces][R];  // score scale of each row, log2 domain (read four at a time)
-  int lim[kFewPieces][R];           // last key position that the row sees
+  int near[kFewPieces][R];          // the row sees the keys at least this far from the sequence's end
   // per softmax warp, for its warpgroup's 16 rows (every warp keeps its own copy):
   alignas(16) float off[C::kSoftmaxWarps][16];  // 7 - m (read four at a time)
   float alpha[C::kSoftmaxWarps][16];  // factor of a moved reference; v_scale / l at the end
@@ -105,8 +107,8 @@ struct __align__(1024) FewSmem {
   uint64_t vote[C::kWgs], sync[C::kWgs];
   int moved[C::kWgs];               // last tile with a score that moves a reference
   uint32_t bad[kFewBad];            // blocks of a tile outside the pool
-  long long chunk, begin, end, rest;  // the CTA's stretch; length into its first sequence
-  int b0;                           // that sequence
+  int chunk, begin, end;            // the group's stretch of the line (int: the host bounds its length)
+  int b0, rest;                     // the sequence that it begins in, and where in it
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -115,7 +117,7 @@ struct FewParams {
   Params p;        // o, lse, cu_q, block_table, seq_lens, sizes, scales; tok_tile = R / G
   float* part_o;   // [2 * CTAs][R][128]: pieces of cut sequences
   float* part_lse; // [2 * CTAs][R]
-  int2* meta;      // [B]: first and last group of the sequence, equal when nothing is to be merged
+  int4* meta;      // [B]: first and last group of the sequence (equal: nothing to merge), qoff, T
   int chunk;       // length of a group's stretch; 0: the line dealt out evenly
   int seq_tiles;   // length of every sequence; 0: its tiles and kFewPieceCost
 };
@@ -142,20 +144,20 @@ __device__ __forceinline__ int few_extent(const FewParams& f, const FewSeq& q) {
 // The walk over a group's stretch of the line.
 struct FewWalk {
   int b, lo;            // next piece: sequence b from its place lo on
-  long long pos, end;   // place on the line, end of the stretch
+  int pos, end;         // place on the line, end of the stretch
   // the piece, of sequence pb
   FewSeq q;
   int pb;
   int j0, n;            // first tile, tiles
   bool whole, last;     // the whole sequence; its end
-  long long seq_pos;    // where the sequence begins
+  int seq_pos;          // where the sequence begins
 
   __device__ __forceinline__ bool next(const FewParams& f) {
     for (; pos < end && b < f.p.B; ++b) {
       q = few_seq(f.p, b);
       const int extent = few_extent(f, q);
       if (extent == 0) continue;
-      const int hi = static_cast<int>(min(static_cast<long long>(extent), lo + (end - pos)));
+      const int hi = min(extent, lo + (end - pos));
       const int cost = f.seq_tiles > 0 ? 0 : kFewPieceCost;  // the first places hold no tile
       j0 = max(lo - cost, 0);
       n = max(min(hi - cost, q.tiles) - j0, 0);
@@ -172,7 +174,7 @@ struct FewWalk {
 };
 
 template <int R>
-constexpr size_t few_smem_bytes() { return sizeof(FewSmem<R>) + 1024; }
+constexpr size_t few_smem_bytes() { return sizeof(FewSmem<R>); }
 
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -206,8 +208,10 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
                     const __nv_bfloat16* __restrict__ q, const __grid_constant__ FewParams f) {
   using C = FewConfig<R>;
   const Params& p = f.p;
-  extern __shared__ uint8_t smem_raw[];
-  FewSmem<R>& sm = *reinterpret_cast<FewSmem<R>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // Used as it is: an address computed from it would lose its state space, and
+  // every access would be a generic one with a 64-bit address.
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  FewSmem<R>& sm = *reinterpret_cast<FewSmem<R>*>(smem_raw);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
@@ -252,7 +256,7 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
   // Length of the line and, with it, this group's stretch.  Sequences without a
   // key are dealt out too: their rows become o = 0, lse = -inf.
   if (warp == 0) {
-    long long total = 0;
+    int total = 0;
 #pragma unroll 4
     for (int b = lane; b < p.B; b += 32) {
       const FewSeq s = few_seq(p, b);
@@ -260,7 +264,7 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
       if (cta == 0 && (raw < 0 || raw > p.max_blocks * 16)) atomicOr(&g_devstatus, kDevStatusBadSeqLen);
       total += few_extent(f, s);
       if (s.tiles == 0 && b % gridDim.x == cta) {
-        f.meta[b] = make_int2(0, 0);
+        f.meta[b] = make_int4(0, 0, 0, 0);
         for (int t = 0; t < s.T && s.qoff + t < p.total_q; ++t)
           for (int h = 0; h < p.Hq; ++h) {
             const size_t tok = static_cast<size_t>(s.qoff) + t;
@@ -272,38 +276,33 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    const long long even = (total + groups - 1) / groups;
-    const long long chunk = f.chunk > 0 ? f.chunk : even > kFewMinChunk ? even : kFewMinChunk;
-    const long long begin = chunk * group;
+    const int even = (total + groups - 1) / groups;
+    const int chunk = f.chunk > 0 ? f.chunk : max(even, kFewMinChunk);
+    // past the line's end: the product may be larger than an int
+    const int begin = static_cast<int>(min(static_cast<long long>(chunk) * group, static_cast<long long>(total)));
     // the sequence that the stretch begins in
-    long long before = 0;
-    int b0 = p.B;
-    long long rest = 0;
+    int before = 0, b0 = p.B, rest = 0;
     for (int base = 0; base < p.B && b0 == p.B; base += 32) {
       const int b = base + lane;
-      long long len = 0;
-      if (b < p.B) {
-        const FewSeq s = few_seq(p, b);
-        len = few_extent(f, s);
-      }
-      long long incl = len;
+      const int len = b < p.B ? few_extent(f, few_seq(p, b)) : 0;
+      int incl = len;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
       const uint32_t m = __ballot_sync(0xffffffffu, begin < before + incl);
       if (m != 0) {
         const int w = __ffs(m) - 1;
         b0 = base + w;
-        rest = begin - before - __shfl_sync(0xffffffffu, incl - len, w);  // places into sequence b0
+        rest = begin - before - __shfl_sync(0xffffffffu, incl - len, w);
       }
       before += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) {
       sm.chunk = chunk;
       sm.begin = begin;
-      sm.end = min(begin + chunk, total);
+      sm.end = begin + min(chunk, total - begin);
       sm.b0 = b0;
       sm.rest = rest;
     }
@@ -330,18 +329,55 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
     walk.pos = sm.begin;
     walk.end = sm.end;
     walk.b = sm.b0;
-    walk.lo = static_cast<int>(sm.rest);
+    walk.lo = sm.rest;
     int issued = 0;
     const uint64_t pol = l2_policy_evict_first();  // every byte is read once
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const bool more = walk.next(f);
+      const int32_t* table = p.block_table + static_cast<size_t>(walk.pb) * p.max_blocks;
+      const int nblk_all = more ? (walk.q.S + 15) / 16 : 0;
+      const int n = more ? walk.n : 0;
+      int id_next = lane < 8 && n > 0 && walk.j0 * 8 + lane < nblk_all ? __ldg(table + walk.j0 * 8 + lane) : 0;
+      auto copy_tile = [&](int j) {
+        const int blk0 = (walk.j0 + j) * 8;
+        const int nblk = min(8, nblk_all - blk0);
+        const int id = id_next;
+        if (j + 1 < n) id_next = lane < 8 && blk0 + 8 + lane < nblk_all ? __ldg(table + blk0 + 8 + lane) : 0;
+        const bool in_pool = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
+        const uint32_t bad = __ballot_sync(0xffffffffu, lane < nblk && !in_pool);
+        if (bad && lane == 0) atomicOr(&g_devstatus, kDevStatusBadBlock);
+        const uint32_t bytes = static_cast<uint32_t>(nblk - __popc(bad)) * 16 * kD;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const int t = 2 * jt + kv, s = t % C::kSlots;
+          if (lane == 0) {
+            ok = mbar_wait(&sm.empty[s], ((t / C::kSlots) & 1) ^ 1, abort_flag);
+            if (ok) {
+              if (kv == 0) sm.bad[jt % kFewBad] = bad;
+              mbar_arrive_expect_tx(&sm.full[s], bytes);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) return;
+          if (lane < nblk && in_pool)
+            tma_load_2d_hint(sm.ring[s] + lane * 16 * 128, kv ? &tmV : &tmK, &sm.full[s], hk * kD, id * 16, pol);
+          issued = t + 1;
+        }
+        ++jt;
+      };
+      // The first piece's first copies go before its q (the ring is empty then).
+      int j = 0;
+      if (i == 0)
+        for (; j < min(2, n) && ok; ++j) copy_tile(j);
+      if (!ok) break;
+      // the piece's q and description, once the piece two before is done
       const int slot = i % kFewPieces;
       ok = __all_sync(0xffffffffu, mbar_wait(&sm.piece_free[slot], ((i / kFewPieces) & 1) ^ 1, abort_flag));
       if (!ok) break;
       if (more && walk.n > 0) {
         // q rows to e4m3 hi and lo terms: eight lanes a row, 16 elements each
-        constexpr int kBatch = 4;  // rows of four in flight
+        constexpr int kBatch = R <= 16 ? 4 : 2;  // rows of four in flight
         for (int r0 = 0; r0 < R; r0 += 4 * kBatch) {
           uint32_t w[kBatch][8];
 #pragma unroll
@@ -373,9 +409,7 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
             *reinterpret_cast<uint4*>(sm.q[slot] + (R + r) * 128 + ((u ^ (r & 7)) << 4)) = lo;
             if (u == 0) {
               sm.sl2[slot][r] = row_score_scale(p.scale_log2, rs);
-              sm.lim[slot][r] = r >= walk.q.T * p.G ? 0x7fffffff
-                                : p.causal          ? walk.q.S - walk.q.T + r / p.G
-                                                    : walk.q.S - 1;
+              sm.near[slot][r] = r >= walk.q.T * p.G ? INT_MIN : p.causal ? walk.q.T - r / p.G : 1;
             }
           }
         }
@@ -391,40 +425,12 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
         pc.S = walk.q.S;
         pc.whole = walk.whole;
         pc.last = walk.last;
-        pc.g0 = more ? static_cast<int>(walk.seq_pos / sm.chunk) : 0;
+        pc.g0 = more ? walk.seq_pos / sm.chunk : 0;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.piece_full[slot]);
       if (!more) break;
-      const int32_t* table = p.block_table + static_cast<size_t>(walk.pb) * p.max_blocks;
-      const int nblk_all = (walk.q.S + 15) / 16;
-      int id_next = lane < 8 && walk.n > 0 && walk.j0 * 8 + lane < nblk_all ? __ldg(table + walk.j0 * 8 + lane) : 0;
-      for (int j = 0; j < walk.n && ok; ++j, ++jt) {
-        const int blk0 = (walk.j0 + j) * 8;
-        const int nblk = min(8, nblk_all - blk0);
-        const int id = id_next;
-        if (j + 1 < walk.n) id_next = lane < 8 && blk0 + 8 + lane < nblk_all ? __ldg(table + blk0 + 8 + lane) : 0;
-        const bool in_pool = static_cast<unsigned>(id) < static_cast<unsigned>(p.num_blocks);
-        const uint32_t bad = __ballot_sync(0xffffffffu, lane < nblk && !in_pool);
-        if (bad && lane == 0) atomicOr(&g_devstatus, kDevStatusBadBlock);
-        const uint32_t bytes = static_cast<uint32_t>(nblk - __popc(bad)) * 16 * kD;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int t = 2 * jt + kv, s = t % C::kSlots;
-          if (lane == 0) {
-            ok = mbar_wait(&sm.empty[s], ((t / C::kSlots) & 1) ^ 1, abort_flag);
-            if (ok) {
-              if (kv == 0) sm.bad[jt % kFewBad] = bad;
-              mbar_arrive_expect_tx(&sm.full[s], bytes);
-            }
-          }
-          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-          if (!ok) break;
-          if (lane < nblk && in_pool)
-            tma_load_2d_hint(sm.ring[s] + lane * 16 * 128, kv ? &tmV : &tmK, &sm.full[s], hk * kD, id * 16, pol);
-          issued = t + 1;
-        }
-      }
+      for (; j < n && ok; ++j) copy_tile(j);
     }
     if (lane == 0 && *abort_flag)  // let the copies already issued land before shared memory is released
       for (int i = max(0, issued - C::kSlots); i < issued; ++i)
@@ -519,7 +525,7 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
     // After a wait that gave up a warp goes on without waiting (the output is
     // then undefined and not written).
     bool ok = true;
-    int syncs = 0, votes = 0;
+    int syncs = 0;
     auto sync_wg = [&]() {  // the warpgroup's four warps, with a bounded wait
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.sync[wg]);
@@ -527,38 +533,59 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
       ++syncs;
     };
     for (int i = 0, piece = 0; ok; ++i) {
-      FewPiece pc;
-      ok = __all_sync(0xffffffffu, take_piece(i, pc));
+      ok = __all_sync(0xffffffffu, mbar_wait(&sm.piece_full[i % kFewPieces], (i / kFewPieces) & 1, abort_flag));
+      const FewPiece& pc = sm.piece[i % kFewPieces];  // read where it is needed, not held in registers
       if (!ok || pc.b < 0) break;
-      const int T = pc.T, S = pc.S, qoff = pc.qoff, n = pc.n;
-      const int rows = T * p.G;
-      const bool whole = pc.whole != 0;
-      const int slot = 2 * cta + (pc.last ? 0 : 1);  // of a cut sequence's piece
-      if (pc.last && hk == 0 && threadIdx.x == 0) f.meta[pc.b] = make_int2(pc.g0, group);
+      const int n = pc.n;
+      if (pc.last && hk == 0 && threadIdx.x == 0) f.meta[pc.b] = make_int4(pc.g0, group, pc.qoff, pc.T);
       if (n == 0) {  // nothing on this piece: the merge skips it
-        if (threadIdx.x < rows) f.part_lse[static_cast<size_t>(slot) * R + threadIdx.x] = -INFINITY;
+        if (threadIdx.x < pc.T * p.G) f.part_lse[static_cast<size_t>(2 * cta + (pc.last ? 0 : 1)) * R + threadIdx.x] = -INFINITY;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.piece_free[i % kFewPieces]);
         continue;
       }
       const float* const sl2 = sm.sl2[i % kFewPieces] + h0;
-      const int* const lim = sm.lim[i % kFewPieces] + h0;
+      const int* const near = sm.near[i % kFewPieces] + h0;
       if (lane < 16) off[lane] = kFewUnseen;
       __syncwarp();
 
       float2 l[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) l[e] = make_float2(0.f, 0.f);
-      const int first_lim = p.causal ? S - T : S - 1;  // last key that every row sees
-      int pos = pc.j0 * kBN + k;                         // this thread's key
-      for (int j = 0; j < n; ++j, ++jt, pos += kBN) {
+      int left = pc.S - pc.j0 * kBN - k;     // this thread's key: how far from the sequence's end
+      const int all_see = p.causal ? pc.T : 1;  // keys at least this far are seen by every row
+      // Before or after the vote's answer: with two warpgroups a thread has 96
+      // registers, which do not hold sums, weights and terms at once.
+      constexpr bool kEarly = R == 16;
+      for (int j = 0; j < n; ++j, ++jt, left -= kBN) {
         const int buf = jt & 1;
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[buf], (jt >> 1) & 1, abort_flag));
         tc_fence_after();
-        const bool dead = pos >= S || ((sm.bad[jt % kFewBad] >> (k >> 4)) & 1u);
-        const bool masked = __any_sync(0xffffffffu, dead || pos > first_lim);
+        const bool dead = left <= 0 || ((sm.bad[jt % kFewBad] >> (k >> 4)) & 1u);
+        const bool masked = __any_sync(0xffffffffu, dead || left < all_see);
         float2 w[8];        // scores, exponents, weights
         uint32_t pt[4][4];  // the weights' e5m2 terms, four rows to a word
+        auto weights = [&]() {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float2 &p0 = w[2 * i], &p1 = w[2 * i + 1];
+            p0 = make_float2(ex2_approx(p0.x), ex2_approx(p0.y));
+            p1 = make_float2(ex2_approx(p1.x), ex2_approx(p1.y));
+            uint32_t a = pack_f16x2(p0.x, p0.y), c = pack_f16x2(p1.x, p1.y);
+            if constexpr (!kEarly) {
+              l[2 * i] = __fadd2_rn(l[2 * i], p0);
+              l[2 * i + 1] = __fadd2_rn(l[2 * i + 1], p1);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              pt[t][i] = prmt(a, c, 0x7531);  // the four top bytes
+              if (t < 3) {
+                a = hsub2(a, a & 0xff00ff00u);
+                c = hsub2(c, c & 0xff00ff00u);
+              }
+            }
+          }
+        };
         // The first tile sets the references; a later one is done again in the
         // rare case that one of its scores moves a reference.
         for (bool update = j == 0;; update = true) {
@@ -573,8 +600,8 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
           if (masked) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              if (dead || pos > lim[2 * i]) w[i].x = -INFINITY;
-              if (dead || pos > lim[2 * i + 1]) w[i].y = -INFINITY;
+              if (dead || left < near[2 * i]) w[i].x = -INFINITY;
+              if (dead || left < near[2 * i + 1]) w[i].y = -INFINITY;
             }
           }
           if (update) {
@@ -614,8 +641,7 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
               l[i].y *= alpha[2 * i + 1];
             }
           }
-          // exponents, and whether one of them moves its row's reference; the
-          // answer is awaited only after the exponentials
+          // exponents, and whether one of them moves its row's reference
           float top = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 8; i += 2) {
@@ -630,31 +656,20 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.vote[wg]);
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float2 &p0 = w[2 * i], &p1 = w[2 * i + 1];
-            p0 = make_float2(ex2_approx(p0.x), ex2_approx(p0.y));
-            p1 = make_float2(ex2_approx(p1.x), ex2_approx(p1.y));
-            uint32_t a = pack_f16x2(p0.x, p0.y), c = pack_f16x2(p1.x, p1.y);
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              pt[t][i] = prmt(a, c, 0x7531);  // the four top bytes
-              if (t < 3) {
-                a = hsub2(a, a & 0xff00ff00u);
-                c = hsub2(c, c & 0xff00ff00u);
-              }
-            }
-          }
+          if constexpr (kEarly) weights();
           if (update) break;
-          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.vote[wg], votes & 1, abort_flag));
-          ++votes;
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.vote[wg], (jt - piece - 1) & 1, abort_flag));
           if (!ok || *static_cast<volatile int*>(&sm.moved[wg]) != jt) break;
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.s_free[buf]);
+        if constexpr (kEarly) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) l[i] = __fadd2_rn(l[i], w[i]);
+          for (int i = 0; i < 8; ++i) l[i] = __fadd2_rn(l[i], w[i]);
+        } else {
+          weights();
+        }
         // the P buffer's last readers: the tile before; the piece before, which
         // staged its output there
         if (ok && jt >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free, (jt - 1) & 1, abort_flag));
@@ -682,6 +697,9 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
       }
 
       // Row sums over the 128 keys, then O^T / l.
+      const int rows = pc.T * p.G, qoff = pc.qoff;
+      const bool whole = pc.whole != 0;
+      const int slot = 2 * cta + (pc.last ? 0 : 1);  // of a cut sequence's piece
       {
         const float v = warp_reduce16<false>(l, lane);
         if (!(lane & 1)) sm.sum[warp][lane >> 1] = v;
@@ -771,11 +789,10 @@ __global__ void __launch_bounds__(128) prefill_fp8_few_merge(const __grid_consta
   grid_dependency_wait();
   grid_launch_dependents();
   const int b = blockIdx.x / p.Hkv, hk = blockIdx.x % p.Hkv;
-  const int2 m = f.meta[b];
+  const int4 m = f.meta[b];
   if (m.x == m.y) return;  // finished on one stretch
-  const FewSeq q = few_seq(p, b);
-  const int tok = q.qoff + r / p.G;
-  if (r >= q.T * p.G || tok >= p.total_q) return;  // (the whole CTA when it has one row)
+  const int tok = m.z + r / p.G;
+  if (r >= m.w * p.G || tok >= p.total_q) return;  // (the whole CTA when it has one row)
   const int head = hk * p.G + r % p.G;
   const int pieces = m.y - m.x + 1;
   auto slot_row = [&](int i) {

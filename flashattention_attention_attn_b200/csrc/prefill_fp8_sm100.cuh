@@ -87,7 +87,7 @@ struct __align__(1024) Smem {
   int abort_flag;
 };
 
-constexpr size_t smem_bytes() { return sizeof(Smem) + 1024; }
+constexpr size_t smem_bytes() { return sizeof(Smem); }
 
 struct Params {
   __nv_bfloat16* o;            // [total_q, Hq, 128]
@@ -164,8 +164,10 @@ __device__ __forceinline__ int key_tiles(int t0, int n, int T, int S, int causal
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_fp8_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const Params p) {
-  extern __shared__ uint8_t smem_raw[];
-  Smem& sm = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // Used as it is: an address computed from it would lose its state space, and
+  // every access would be a generic one with a 64-bit address.
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   // blockIdx.x = (item, range, kv head), the kv head fastest
