@@ -106,9 +106,23 @@ def _ptr(x) -> int | None:
     return int(x)
 
 
+def _pointers(*xs):
+    """Device pointers for a call on the current device; a tensor that lives
+    elsewhere (another GPU, the host) is refused."""
+    dev = torch.cuda.current_device()
+    out = []
+    for x in xs:
+        if isinstance(x, torch.Tensor):
+            if x.get_device() != dev:
+                raise ValueError(f"a tensor on {x.device} in a call on cuda:{dev} (the current device)")
+            x = x.data_ptr() or None
+        out.append(x)
+    return out
+
+
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle alone: a torch.cuda.Stream object costs 3 us a call, this 0.3
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -243,10 +257,10 @@ def paged_cache_plan(cached_lens, new_lens, free_blocks, pos_offsets, B, num_fre
                      block_table, seq_lens, cu_seqlens_q, slot_map, positions, blocks_taken, stream=None) -> None:
     """Block-table entries, slots, positions and prefix sums of a step's new
     tokens from the requests' lengths (see attn.h)."""
-    rc = library().paged_cache_plan(_ptr(cached_lens), _ptr(new_lens), _ptr(free_blocks), _ptr(pos_offsets), int(B),
-                                    int(num_free), int(block_size), int(max_blocks), int(max_tokens),
-                                    _ptr(block_table), _ptr(seq_lens), _ptr(cu_seqlens_q), _ptr(slot_map),
-                                    _ptr(positions), _ptr(blocks_taken), _stream(stream))
+    ins = _pointers(cached_lens, new_lens, free_blocks, pos_offsets)
+    outs = _pointers(block_table, seq_lens, cu_seqlens_q, slot_map, positions, blocks_taken)
+    rc = library().paged_cache_plan(*ins, int(B), int(num_free), int(block_size), int(max_blocks), int(max_tokens), *outs,
+                                    _stream(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "paged_cache_plan")
 
@@ -281,28 +295,44 @@ def _axis_bytes(freq_axis, rot_dim) -> bytes | None:
     return axes
 
 
+def _rope(name, q, k, positions, inv_freq, freq_axis, n_tokens, Hq, Hkv, d, rot_dim, num_axes, pos_stride, q_stride,
+          k_stride, adjacent, q_out, k_out, q_out_stride, k_out_stride, stream) -> None:
+    axes = _axis_bytes(freq_axis, rot_dim)
+    q, k, positions, inv_freq, q_out, k_out = _pointers(q, k, positions, inv_freq, q_out, k_out)
+    rc = getattr(library(), name)(q, k, positions, inv_freq, axes, int(n_tokens), int(Hq), int(Hkv), int(d), int(rot_dim),
+                                  int(num_axes), int(pos_stride), int(q_stride), int(k_stride), int(bool(adjacent)),
+                                  q_out, k_out, int(q_out_stride), int(k_out_stride), _stream(stream))
+    if rc != ATTN_OK:
+        raise AttnError(rc, name)
+
+
 def rope_axes_fwd(q, k, positions, inv_freq, freq_axis, n_tokens, Hq, Hkv, d, rot_dim, num_axes, pos_stride, q_stride,
                   k_stride, adjacent, q_out, k_out, q_out_stride, k_out_stride, stream=None) -> None:
     """Rotary positions with several axes (see attn.h).  freq_axis: bytes or
     ints, the axis of each of the rot_dim / 2 pairs (rope_axis_map), or None."""
-    rc = library().rope_axes_fwd(_ptr(q), _ptr(k), _ptr(positions), _ptr(inv_freq), _axis_bytes(freq_axis, rot_dim),
-                                 int(n_tokens), int(Hq), int(Hkv), int(d), int(rot_dim), int(num_axes),
-                                 int(pos_stride), int(q_stride), int(k_stride), int(bool(adjacent)), _ptr(q_out),
-                                 _ptr(k_out), int(q_out_stride), int(k_out_stride), _stream(stream))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "rope_axes_fwd")
+    _rope("rope_axes_fwd", q, k, positions, inv_freq, freq_axis, n_tokens, Hq, Hkv, d, rot_dim, num_axes, pos_stride,
+          q_stride, k_stride, adjacent, q_out, k_out, q_out_stride, k_out_stride, stream)
 
 
 def rope_axes_bwd(dq_out, dk_out, positions, inv_freq, freq_axis, n_tokens, Hq, Hkv, d, rot_dim, num_axes, pos_stride,
                   dq_out_stride, dk_out_stride, adjacent, dq, dk, dq_stride, dk_stride, stream=None) -> None:
     """Gradient of rope_axes_fwd (see attn.h)."""
-    rc = library().rope_axes_bwd(_ptr(dq_out), _ptr(dk_out), _ptr(positions), _ptr(inv_freq),
-                                 _axis_bytes(freq_axis, rot_dim), int(n_tokens), int(Hq), int(Hkv), int(d),
-                                 int(rot_dim), int(num_axes), int(pos_stride), int(dq_out_stride),
-                                 int(dk_out_stride), int(bool(adjacent)), _ptr(dq), _ptr(dk), int(dq_stride),
-                                 int(dk_stride), _stream(stream))
+    _rope("rope_axes_bwd", dq_out, dk_out, positions, inv_freq, freq_axis, n_tokens, Hq, Hkv, d, rot_dim, num_axes,
+          pos_stride, dq_out_stride, dk_out_stride, adjacent, dq, dk, dq_stride, dk_stride, stream)
+
+
+def _rope_append(name, q, k, v, positions, inv_freq, freq_axis, slot_map, n_tokens, Hq, Hkv, d, rot_dim, num_axes,
+                 pos_stride, q_stride, k_stride, v_stride, adjacent, block_size, num_blocks, scales, q_out, k_cache,
+                 v_cache, stream) -> None:
+    axes = _axis_bytes(freq_axis, rot_dim)
+    q, k, v, positions, inv_freq, slot_map, q_out, k_cache, v_cache = _pointers(
+        q, k, v, positions, inv_freq, slot_map, q_out, k_cache, v_cache)
+    rc = getattr(library(), name)(q, k, v, positions, inv_freq, axes, slot_map, int(n_tokens), int(Hq), int(Hkv), int(d),
+                                  int(rot_dim), int(num_axes), int(pos_stride), int(q_stride), int(k_stride),
+                                  int(v_stride), int(bool(adjacent)), int(block_size), int(num_blocks), *scales, q_out,
+                                  k_cache, v_cache, _stream(stream))
     if rc != ATTN_OK:
-        raise AttnError(rc, "rope_axes_bwd")
+        raise AttnError(rc, name)
 
 
 def rope_axes_paged_append(q, k, v, positions, inv_freq, freq_axis, slot_map, n_tokens, Hq, Hkv, d, rot_dim, num_axes,
@@ -310,40 +340,28 @@ def rope_axes_paged_append(q, k, v, positions, inv_freq, freq_axis, slot_map, n_
                            v_cache, stream=None) -> None:
     """rope_axes_fwd of q and k, with k and v written into the paged bf16
     cache at slot_map (see attn.h)."""
-    rc = library().rope_axes_paged_append(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(inv_freq),
-                                          _axis_bytes(freq_axis, rot_dim), _ptr(slot_map), int(n_tokens), int(Hq),
-                                          int(Hkv), int(d), int(rot_dim), int(num_axes), int(pos_stride),
-                                          int(q_stride), int(k_stride), int(v_stride), int(bool(adjacent)),
-                                          int(block_size), int(num_blocks), _ptr(q_out), _ptr(k_cache),
-                                          _ptr(v_cache), _stream(stream))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "rope_axes_paged_append")
+    _rope_append("rope_axes_paged_append", q, k, v, positions, inv_freq, freq_axis, slot_map, n_tokens, Hq, Hkv, d,
+                 rot_dim, num_axes, pos_stride, q_stride, k_stride, v_stride, adjacent, block_size, num_blocks, (), q_out,
+                 k_cache, v_cache, stream)
 
 
 def rope_axes_paged_append_fp8(q, k, v, positions, inv_freq, freq_axis, slot_map, n_tokens, Hq, Hkv, d, rot_dim,
                                num_axes, pos_stride, q_stride, k_stride, v_stride, adjacent, block_size, num_blocks,
                                k_scale, v_scale, q_out, k_cache, v_cache, stream=None) -> None:
     """rope_axes_paged_append into an FP8 e4m3 cache with per-tensor scales (see attn.h)."""
-    rc = library().rope_axes_paged_append_fp8(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(inv_freq),
-                                              _axis_bytes(freq_axis, rot_dim), _ptr(slot_map), int(n_tokens),
-                                              int(Hq), int(Hkv), int(d), int(rot_dim), int(num_axes),
-                                              int(pos_stride), int(q_stride), int(k_stride), int(v_stride),
-                                              int(bool(adjacent)), int(block_size), int(num_blocks), float(k_scale),
-                                              float(v_scale), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
-                                              _stream(stream))
-    if rc != ATTN_OK:
-        raise AttnError(rc, "rope_axes_paged_append_fp8")
+    _rope_append("rope_axes_paged_append_fp8", q, k, v, positions, inv_freq, freq_axis, slot_map, n_tokens, Hq, Hkv, d,
+                 rot_dim, num_axes, pos_stride, q_stride, k_stride, v_stride, adjacent, block_size, num_blocks,
+                 (float(k_scale), float(v_scale)), q_out, k_cache, v_cache, stream)
 
 
 def paged_attn_prefill_fp8(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, B, Hq, Hkv, d, block_size,
                            max_blocks, max_seqlen_q, total_q, causal, scale, k_scale, v_scale, num_splits, o, lse,
                            stream=None) -> None:
     """Chunked prefill against an FP8 e4m3 paged cache with per-tensor scales (see attn.h)."""
-    rc = library().paged_attn_prefill_fp8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
-                                          _ptr(cu_seqlens_q), int(B), int(Hq), int(Hkv), int(d), int(block_size),
-                                          int(max_blocks), int(max_seqlen_q), int(total_q), int(bool(causal)),
-                                          float(scale), float(k_scale), float(v_scale), int(num_splits), _ptr(o),
-                                          _ptr(lse), _stream(stream))
+    ptrs = _pointers(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, o, lse)
+    rc = library().paged_attn_prefill_fp8(*ptrs[:6], int(B), int(Hq), int(Hkv), int(d), int(block_size), int(max_blocks),
+                                          int(max_seqlen_q), int(total_q), int(bool(causal)), float(scale),
+                                          float(k_scale), float(v_scale), int(num_splits), *ptrs[6:], _stream(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "paged_attn_prefill_fp8")
 
@@ -352,12 +370,11 @@ def paged_attn_prefill_fp8_checked(q, k_cache, v_cache, block_table, seq_lens, c
                                    max_blocks, num_blocks, max_seqlen_q, total_q, causal, scale, k_scale, v_scale,
                                    num_splits, o, lse, stream=None) -> None:
     """paged_attn_prefill_fp8 for a pool of num_blocks blocks (see attn.h)."""
-    rc = library().paged_attn_prefill_fp8_checked(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-                                                  _ptr(seq_lens), _ptr(cu_seqlens_q), int(B), int(Hq), int(Hkv),
-                                                  int(d), int(block_size), int(max_blocks), int(num_blocks),
-                                                  int(max_seqlen_q), int(total_q), int(bool(causal)), float(scale),
-                                                  float(k_scale), float(v_scale), int(num_splits), _ptr(o), _ptr(lse),
-                                                  _stream(stream))
+    ptrs = _pointers(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, o, lse)
+    rc = library().paged_attn_prefill_fp8_checked(*ptrs[:6], int(B), int(Hq), int(Hkv), int(d), int(block_size),
+                                                  int(max_blocks), int(num_blocks), int(max_seqlen_q), int(total_q),
+                                                  int(bool(causal)), float(scale), float(k_scale), float(v_scale),
+                                                  int(num_splits), *ptrs[6:], _stream(stream))
     if rc != ATTN_OK:
         raise AttnError(rc, "paged_attn_prefill_fp8_checked")
 

@@ -13,6 +13,14 @@ give output shapes without running anything) and with CUDA-graph capture.
     o_part, lse_part = torch.ops.fa_b200.paged_attn_decode_partial(q, k_cache, v_cache, block_table, seq_lens,
                                                                    num_splits)
     o = torch.ops.fa_b200.attn_lse_merge(o_parts, lse_parts)
+    seq_lens, cu_seqlens_q, slot_map, positions, blocks_taken = torch.ops.fa_b200.paged_cache_plan(
+        block_table, cached_lens, new_lens, free_blocks, pos_offsets, max_tokens)
+    q, k = torch.ops.fa_b200.rope_axes(q, k, positions, inv_freq, freq_axis, adjacent)    # differentiable
+    q = torch.ops.fa_b200.rope_axes_paged_append(q, k, v, positions, inv_freq, freq_axis, slot_map, adjacent,
+                                                 k_cache, v_cache)
+    q = torch.ops.fa_b200.rope_axes_paged_append_fp8(..., k_scale, v_scale)
+    o, lse = torch.ops.fa_b200.paged_attn_prefill_fp8(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q,
+                                                      max_seqlen_q, causal, scale, k_scale, v_scale, num_splits)
 
 The op bodies only allocate the outputs and call the library on the current
 stream; there is no other path.  Shapes follow include/attn.h:
@@ -24,6 +32,11 @@ block_table [B,max_blocks], seq_lens [B] -> o [B,Hq,d];
 partial decode (the keys held here, the pool size read from the cache
 shape) -> o_part [B,Hq,d] fp32, lse_part [B,Hq] fp32; merge of R partials
 o_parts [R,B,Hq,d], lse_parts [R,B,Hq] -> o [B,Hq,d] bf16.
+Plan: block_table [B,max_blocks] is updated in place, the other outputs are
+new; pos_offsets may be None.  Rotary: q [n,Hq,d], k [n,Hkv,d] (rows of heads
+may lie further apart, as columns of a fused projection do), positions
+[axes,n] int32, inv_freq [rot/2] fp32, freq_axis a list of rot/2 axes (empty:
+axis 0); the caches are written in place.
 """
 
 from __future__ import annotations
@@ -158,3 +171,176 @@ def attn_lse_merge(o_parts: torch.Tensor, lse_parts: torch.Tensor) -> torch.Tens
 @attn_lse_merge.register_fake
 def _(o_parts, lse_parts):
     return o_parts.new_empty(o_parts.shape[1:], dtype=torch.bfloat16)
+
+
+def _rows(x: torch.Tensor) -> torch.Tensor:
+    """x [n, H, d] with the heads of a row side by side, copied only if they are not."""
+    if x.stride(-1) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]) or x.stride(0) % 8 or x.data_ptr() % 16:
+        return x.contiguous()
+    return x
+
+
+_BF16, _INT32, _FP32 = (torch.bfloat16,), (torch.int32,), (torch.float32,)
+_FP8 = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _need(packed: bool, dtypes, **tensors) -> None:
+    """The types that the entry points read behind their pointers and, packed, no gaps."""
+    for name, x in tensors.items():
+        if x is None:
+            continue
+        if x.dtype not in dtypes:
+            raise ValueError(f"{name} is {x.dtype}, not {' or '.join(str(t) for t in dtypes)}")
+        if packed and not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _stride(x: torch.Tensor) -> int:
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def _positions(positions: torch.Tensor) -> torch.Tensor:
+    return positions if positions.stride(-1) == 1 or positions.shape[-1] == 1 else positions.contiguous()
+
+
+@torch.library.custom_op("fa_b200::paged_cache_plan", mutates_args=("block_table",))
+def paged_cache_plan(block_table: torch.Tensor, cached_lens: torch.Tensor, new_lens: torch.Tensor,
+                     free_blocks: torch.Tensor, pos_offsets: torch.Tensor | None, max_tokens: int
+                     ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    _need(True, _INT32, block_table=block_table, cached_lens=cached_lens, new_lens=new_lens, free_blocks=free_blocks,
+          pos_offsets=pos_offsets)
+    B, max_blocks = block_table.shape
+    out = [torch.empty(n, device=block_table.device, dtype=torch.int32)
+           for n in (B, B + 1, max_tokens, max_tokens, 1)]
+    seq_lens, cu, slots, positions, taken = out
+    with torch.cuda.device(block_table.device):  # the call is made on, and its stream taken from, the tensors' device
+        _binding.paged_cache_plan(cached_lens, new_lens, free_blocks, pos_offsets, B, free_blocks.numel(), 16, max_blocks,
+                                  max_tokens, block_table, seq_lens, cu, slots, positions, taken)
+    return seq_lens, cu, slots, positions, taken
+
+
+@paged_cache_plan.register_fake
+def _(block_table, cached_lens, new_lens, free_blocks, pos_offsets, max_tokens):
+    B = block_table.shape[0]
+    return tuple(block_table.new_empty(n, dtype=torch.int32) for n in (B, B + 1, max_tokens, max_tokens, 1))
+
+
+def _rope(call, q, k, positions, inv_freq, freq_axis, adjacent):
+    _need(False, _BF16, q=q, k=k)
+    _need(False, _INT32, positions=positions)
+    _need(True, _FP32, inv_freq=inv_freq)
+    n, Hq, d = q.shape
+    Hkv = k.shape[1]
+    q, k, positions = _rows(q), _rows(k), _positions(positions)
+    q_out = torch.empty((n, Hq, d), device=q.device, dtype=q.dtype)
+    k_out = torch.empty((n, Hkv, d), device=q.device, dtype=q.dtype)
+    with torch.cuda.device(q.device):
+        call(q, k, positions, inv_freq, freq_axis or None, n, Hq, Hkv, d, 2 * inv_freq.numel(), positions.shape[0],
+             positions.stride(0), _stride(q), _stride(k), adjacent, q_out, k_out, Hq * d, Hkv * d)
+    return q_out, k_out
+
+
+def _rope_fake(q, k, positions, inv_freq, freq_axis, adjacent):
+    return q.new_empty(q.shape), k.new_empty(k.shape)
+
+
+@torch.library.custom_op("fa_b200::rope_axes", mutates_args=())
+def rope_axes(q: torch.Tensor, k: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, freq_axis: list[int],
+              adjacent: bool) -> tuple[torch.Tensor, torch.Tensor]:
+    return _rope(_binding.rope_axes_fwd, q, k, positions, inv_freq, freq_axis, adjacent)
+
+
+@torch.library.custom_op("fa_b200::rope_axes_bwd", mutates_args=())
+def rope_axes_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
+                  freq_axis: list[int], adjacent: bool) -> tuple[torch.Tensor, torch.Tensor]:
+    return _rope(_binding.rope_axes_bwd, dq_out, dk_out, positions, inv_freq, freq_axis, adjacent)
+
+
+rope_axes.register_fake(_rope_fake)
+rope_axes_bwd.register_fake(_rope_fake)
+
+
+def _rope_setup(ctx, inputs, output):
+    _, _, positions, inv_freq, ctx.freq_axis, ctx.adjacent = inputs
+    ctx.save_for_backward(positions, inv_freq)
+
+
+def _rope_backward(ctx, dq_out, dk_out):
+    positions, inv_freq = ctx.saved_tensors
+    dq, dk = torch.ops.fa_b200.rope_axes_bwd(dq_out, dk_out, positions, inv_freq, ctx.freq_axis, ctx.adjacent)
+    return dq, dk, None, None, None, None
+
+
+rope_axes.register_autograd(_rope_backward, setup_context=_rope_setup)
+
+
+def _append(q, k, v, positions, inv_freq, freq_axis, slot_map, adjacent, k_cache, v_cache, scales):
+    _need(False, _BF16, q=q, k=k, v=v)
+    _need(False, _INT32, positions=positions)
+    _need(True, _INT32, slot_map=slot_map)
+    _need(True, _FP32, inv_freq=inv_freq)
+    _need(True, _FP8 if scales else _BF16, k_cache=k_cache, v_cache=v_cache)
+    n, Hq, d = q.shape
+    Hkv = k.shape[1]
+    q, k, v, positions = _rows(q), _rows(k), _rows(v), _positions(positions)
+    q_out = torch.empty((n, Hq, d), device=q.device, dtype=q.dtype)
+    call = _binding.rope_axes_paged_append_fp8 if scales else _binding.rope_axes_paged_append
+    with torch.cuda.device(q.device):
+        call(q, k, v, positions, inv_freq, freq_axis or None, slot_map, n, Hq, Hkv, d, 2 * inv_freq.numel(),
+             positions.shape[0], positions.stride(0), _stride(q), _stride(k), _stride(v), adjacent, k_cache.shape[1],
+             k_cache.shape[0], *scales, q_out, k_cache, v_cache)
+    return q_out
+
+
+@torch.library.custom_op("fa_b200::rope_axes_paged_append", mutates_args=("k_cache", "v_cache"))
+def rope_axes_paged_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                           inv_freq: torch.Tensor, freq_axis: list[int], slot_map: torch.Tensor, adjacent: bool,
+                           k_cache: torch.Tensor, v_cache: torch.Tensor) -> torch.Tensor:
+    return _append(q, k, v, positions, inv_freq, freq_axis, slot_map, adjacent, k_cache, v_cache, ())
+
+
+@rope_axes_paged_append.register_fake
+def _(q, k, v, positions, inv_freq, freq_axis, slot_map, adjacent, k_cache, v_cache):
+    return q.new_empty(q.shape)
+
+
+@torch.library.custom_op("fa_b200::rope_axes_paged_append_fp8", mutates_args=("k_cache", "v_cache"))
+def rope_axes_paged_append_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                               inv_freq: torch.Tensor, freq_axis: list[int], slot_map: torch.Tensor, adjacent: bool,
+                               k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: float,
+                               v_scale: float) -> torch.Tensor:
+    return _append(q, k, v, positions, inv_freq, freq_axis, slot_map, adjacent, k_cache, v_cache, (k_scale, v_scale))
+
+
+@rope_axes_paged_append_fp8.register_fake
+def _(q, k, v, positions, inv_freq, freq_axis, slot_map, adjacent, k_cache, v_cache, k_scale, v_scale):
+    return q.new_empty(q.shape)
+
+
+@torch.library.custom_op("fa_b200::paged_attn_prefill_fp8", mutates_args=())
+def paged_attn_prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                           seq_lens: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqlen_q: int, causal: bool,
+                           scale: float, k_scale: float, v_scale: float,
+                           num_splits: int) -> tuple[torch.Tensor, torch.Tensor]:
+    _need(False, _BF16, q=q)
+    _need(True, _FP8, k_cache=k_cache, v_cache=v_cache)
+    _need(True, _INT32, block_table=block_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q)
+    q = q.contiguous()
+    total_q, Hq, d = q.shape
+    num_blocks, block_size, Hkv = k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
+    B = cu_seqlens_q.shape[0] - 1
+    o = torch.empty((total_q, Hq, d), device=q.device, dtype=q.dtype)
+    lse = torch.empty((Hq, total_q), device=q.device, dtype=torch.float32)
+    if B > 0:
+        with torch.cuda.device(q.device):
+            _binding.paged_attn_prefill_fp8_checked(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, B, Hq, Hkv,
+                                                    d, block_size, block_table.shape[1], num_blocks, max_seqlen_q,
+                                                    total_q, causal, scale, k_scale, v_scale, num_splits, o, lse)
+    return o, lse
+
+
+@paged_attn_prefill_fp8.register_fake
+def _(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens_q, max_seqlen_q, causal, scale, k_scale, v_scale,
+      num_splits):
+    total_q, Hq, _ = q.shape
+    return q.new_empty(q.shape), q.new_empty((Hq, total_q), dtype=torch.float32)

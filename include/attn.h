@@ -488,8 +488,9 @@ int paged_cache_plan(const int32_t* cached_lens, const int32_t* new_lens, const 
  *   rot_dim on are copied.  The angle is formed in fp64 and reduced there,
  *   cos, sin and the rotation are fp32, the result is rounded once to bf16.
  *   Hq or Hkv may be 0 (its pointers may then be NULL).
- *   Supported: d in {64, 128}; rot_dim % 16 == 0; strides that are multiples
- *   of 8; 16-byte aligned q, k, outputs; sm_100.  n_tokens == 0 is a no-op.
+ *   Supported: d in {64, 128}; rot_dim % 16 == 0; at most 2048 heads a token
+ *   (Hq + 2 Hkv); strides that are multiples of 8; 16-byte aligned q, k,
+ *   outputs; sm_100.  n_tokens == 0 is a no-op.
  *   Errors: ATTN_ERR_INVALID_ARG for null pointers, negative sizes,
  *   num_axes <= 0, rot_dim > d, an axis >= num_axes or a stride smaller than
  *   the row; ATTN_ERR_UNSUPPORTED otherwise outside the supported set.  No
@@ -538,8 +539,9 @@ int rope_axes_paged_append(const void* q, const void* k, const void* v, const in
 
 /*
  * rope_axes_paged_append_fp8 - the same into an FP8 (e4m3) cache: the codes
- * of k_rotated / k_scale and v / v_scale (fp32 quotients, round to nearest
- * even, saturated to +-448; NaN stays NaN).
+ * of k_rotated / k_scale and v / v_scale (fp32 products with the fp32
+ * reciprocals of the scales, round to nearest even, saturated to +-448; NaN
+ * stays NaN).
  *   Supported: d == 128; otherwise as rope_axes_paged_append;
  *   ATTN_ERR_INVALID_ARG also for a scale that is not finite and positive.
  */
