@@ -1081,6 +1081,7 @@ int launch_prefill_fp8_few(const CUtensorMap& mk, const CUtensorMap& mv, const v
     if (groups < 1) groups = 1;
     if (groups > most) groups = most;
   }
+  f.groups = static_cast<int>(groups < 0x3fffffff ? groups : 0x3fffffff);
   const long long grid = groups * p.Hkv;
   const long long line = static_cast<long long>(p.B) * ((f.seq_tiles ? f.seq_tiles : max_tiles) + prefill8::kFewPieceCost);
   if (grid > 0x3fffffffLL || units > 0x7fffffffLL || line > 0x7ff00000LL) return ATTN_ERR_UNSUPPORTED;
@@ -1145,42 +1146,44 @@ int launch_prefill_fp8(const void* q, const void* kc, const void* vc, const int3
     return few == 16 ? launch_prefill_fp8_few<16>(mk, mv, q, p, max_tiles, num_splits, stream, st)
                      : launch_prefill_fp8_few<32>(mk, mv, q, p, max_tiles, num_splits, stream, st);
   const int rows_cta = 2 * p.tok_tile;
-  p.num_mblocks = (max_q + rows_cta - 1) / rows_cta;
-  long long items = static_cast<long long>(p.num_mblocks) * B;
-  if (B <= 32) {
-    const long long bound = (static_cast<long long>(total_q) + static_cast<long long>(B) * (rows_cta - 1)) / rows_cta;
-    if (bound < items) items = bound;
-    p.items = static_cast<int>(items);
+  const int num_mblocks = (max_q + rows_cta - 1) / rows_cta;
+  // units at most: query blocks that exist x kv heads
+  long long units = static_cast<long long>(num_mblocks) * B;
+  const long long bound = (static_cast<long long>(total_q) + static_cast<long long>(B) * (rows_cta - 1)) / rows_cta;
+  if (bound < units) units = bound;
+  units *= Hkv;
+  // Short tables have only short units, which are never cut.
+  if (num_splits <= 0 && max_tiles <= prefill8::kMinCutTiles) num_splits = 1;
+  const int splits_asked = num_splits > 0 ? num_splits : 1;
+  const int chunk = (max_tiles + splits_asked - 1) / splits_asked;
+  const int splits = (max_tiles + chunk - 1) / chunk;
+  p.unit_keys = splits * chunk * prefill8::kBN;
+  p.sms = st->sms;
+  long long grid = units * splits;
+  if (num_splits > 0) {  // every unit counts as num_splits ranges of equal length, a CTA takes one
+    p.stretch = static_cast<long long>(chunk) * prefill8::kBN;
+    p.slots = 1;
+    if (splits > 1) p.num_cuts = static_cast<int>(grid < 0x3fffffff ? grid : 0x3fffffff);
+  } else {
+    p.slots = 2;
+    p.num_cuts = st->sms;
+    if (grid < st->sms) grid = st->sms;
   }
-  // Ranges of key tiles: with fewer units than SMs, as many as fill one wave
-  // when every sequence fills its table row (the host does not know the
-  // lengths).  No range under 4 tiles (512 keys).
-  const long long units = items * Hkv;
-  long long splits = num_splits;
-  if (num_splits <= 0) {
-    splits = units < st->sms ? st->sms / units : 1;
-    if (splits > (max_tiles + 3) / 4) splits = (max_tiles + 3) / 4;
-  }
-  p.chunk = static_cast<int>((max_tiles + splits - 1) / splits);
-  p.splits = (max_tiles + p.chunk - 1) / p.chunk;
-  const long long grid = units * p.splits;
-  const long long merge_grid =
-      (static_cast<long long>(total_q) * Hq + prefill8::kCombineWarps - 1) / prefill8::kCombineWarps;
-  if (grid > 0x7fffffffLL || merge_grid > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
-
+  if (grid > 0x3fffffffLL || max_tiles > (0x7fffffff / prefill8::kBN) / 2) return ATTN_ERR_UNSUPPORTED;
   void* ws = nullptr;
-  if (p.splits > 1) {
-    const size_t rows = static_cast<size_t>(p.splits) * total_q * Hq;
-    if (int rc = workspace(&ws, rows * (D + 1) * sizeof(float), stream, st)) return rc;
+  if (p.num_cuts > 0) {
+    const size_t rows = static_cast<size_t>(p.num_cuts) * p.slots * prefill8::kRows;
+    const size_t bytes = rows * (D + 1) * sizeof(float) + static_cast<size_t>(p.num_cuts) * sizeof(prefill8::Cut);
+    if (int rc = workspace(&ws, bytes, stream, st)) return rc;
     p.part_o = static_cast<float*>(ws);
     p.part_lse = p.part_o + rows * D;
+    p.cuts = reinterpret_cast<prefill8::Cut*>(p.part_lse + rows);
   }
   int rc = launch_pdl(prefill8::prefill_fp8_sm100, dim3(static_cast<unsigned>(grid)), dim3(prefill8::kThreads),
                       prefill8::smem_bytes(), stream, mq, mk, mv, p);
-  if (rc == ATTN_OK && p.splits > 1)
-    rc = launch_pdl(prefill8::prefill_fp8_combine, dim3(static_cast<unsigned>(merge_grid)),
-                    dim3(prefill8::kCombineWarps * 32), 0, stream, static_cast<const float*>(p.part_o),
-                    static_cast<const float*>(p.part_lse), cu_q, p.o, lse, B, Hq, total_q, p.splits);
+  if (rc == ATTN_OK && ws != nullptr)
+    rc = launch_pdl(prefill8::prefill_fp8_merge,
+                    dim3(static_cast<unsigned>(p.num_cuts), prefill8::kRows / prefill8::kMergeRows), dim3(256), 0, stream, p);
   if (ws != nullptr) cudaFreeAsync(ws, stream);
   return rc;
 }

@@ -44,6 +44,11 @@
 // that lies on one stretch is finished there; the pieces of one that a stretch's
 // end cuts go to the workspace (at most two a CTA) and prefill_fp8_few_merge
 // joins them.
+//
+// Measured, G = 4, 8 kv heads: 64 sequences of 4 drafted tokens over 256 to 4096
+// keys 65 us (302 MB of codes, 4.6 TB/s), 8 tokens over 131072 keys 66 us
+// (268 MB, 4.1 TB/s), launch and merge included; with the rows on the lanes of
+// the other kernel 276 and 200 us.
 #pragma once
 
 #include <climits>
@@ -120,6 +125,7 @@ struct FewParams {
   int4* meta;      // [B]: first and last group of the sequence (equal: nothing to merge), qoff, T
   int chunk;       // length of a group's stretch; 0: the line dealt out evenly
   int seq_tiles;   // length of every sequence; 0: its tiles and kFewPieceCost
+  int groups;      // of CTAs
 };
 
 // Tiles of sequence b's keys, 0 when this kernel has no rows of it.
@@ -153,12 +159,16 @@ struct FewWalk {
   int seq_pos;          // where the sequence begins
 
   __device__ __forceinline__ bool next(const FewParams& f) {
+    // The first places hold no tile: an end of a stretch among them counts as
+    // the sequence's beginning, so that no piece is without a tile.
+    const int cost = f.seq_tiles > 0 ? 0 : kFewPieceCost;
     for (; pos < end && b < f.p.B; ++b) {
       q = few_seq(f.p, b);
       const int extent = few_extent(f, q);
       if (extent == 0) continue;
+      if (lo <= cost) pos -= lo, lo = 0;
       const int hi = min(extent, lo + (end - pos));
-      const int cost = f.seq_tiles > 0 ? 0 : kFewPieceCost;  // the first places hold no tile
+      if (hi < extent && hi <= cost) return false;
       j0 = max(lo - cost, 0);
       n = max(min(hi - cost, q.tiles) - j0, 0);
       whole = lo == 0 && hi == extent;
@@ -425,7 +435,7 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
         pc.S = walk.q.S;
         pc.whole = walk.whole;
         pc.last = walk.last;
-        pc.g0 = more ? walk.seq_pos / sm.chunk : 0;
+        pc.g0 = more ? (walk.seq_pos + (f.seq_tiles > 0 ? 0 : kFewPieceCost)) / sm.chunk : 0;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.piece_full[slot]);
@@ -790,9 +800,10 @@ __global__ void __launch_bounds__(128) prefill_fp8_few_merge(const __grid_consta
   grid_launch_dependents();
   const int b = blockIdx.x / p.Hkv, hk = blockIdx.x % p.Hkv;
   const int4 m = f.meta[b];
-  if (m.x == m.y) return;  // finished on one stretch
+  // finished on one stretch (or not written, after a wait that gave up)
+  if (m.x < 0 || m.x >= m.y || m.y >= f.groups) return;
   const int tok = m.z + r / p.G;
-  if (r >= m.w * p.G || tok >= p.total_q) return;  // (the whole CTA when it has one row)
+  if (r >= m.w * p.G || tok < 0 || tok >= p.total_q) return;  // (the whole CTA when it has one row)
   const int head = hk * p.G + r % p.G;
   const int pieces = m.y - m.x + 1;
   auto slot_row = [&](int i) {

@@ -30,9 +30,27 @@
 // CTA = 12 warps: 0-3 and 4-7 softmax of query tile 0 and 1, 8 copies,
 // 9 MMA issue, 10-11 conversion of V.
 //
-// Work split: one CTA per (two query tiles of a sequence, kv head, range of
-// key tiles).  With one range the CTA writes o and lse; otherwise fp32
-// partials and their lse, which prefill_fp8_combine merges.
+// Work split.  A unit is (two query tiles of a sequence, kv head).  The units lie
+// one behind the other on a line and every CTA takes a stretch of it.  Either a
+// stretch is a unit, the longest of a sequence first, and CTAs are handed out as
+// SMs fall free; or one CTA to an SM takes an equal share of all keys, whatever
+// the lengths are, and works through the pieces of units on it (cut_units has the
+// choice, made from the lengths on the device).  There the copies run ahead into
+// the next piece, its q is made ready before the output of the piece before is
+// stored, and its first scores are under way meanwhile.  The pieces of a unit
+// that a stretch's end cuts go to the workspace in fp32 (at most two a stretch)
+// and prefill_fp8_merge joins them.
+//
+// What bounds it: a key iteration (two query tiles x 128 keys) is one chain a
+// query tile, softmax 0.9 us, PV and the next QK 0.55 us, and hand-overs, at
+// 1.95 us; the two tiles fill each other's gaps.  Its MMAs alone take 1.1 us.
+// Slower by 3 to 30% when tried: a share of the exponentials as polynomials on
+// the FMA pipe, P handed over in halves, the tiles' exponentials in strict turns.
+// Straight-line code is kept short (loops over chunks of the output, of q and of
+// V stay rolled): what runs once a piece is fetched cold.
+// Measured, G = 4, 8 kv heads: 2048 tokens at 32k 906 us (1.2 PFLOP/s of 16-bit
+// work), 8 x 512 tokens at .5k to 7.7k 236 us, 4096 tokens from nothing 163 us;
+// 33 sequences of 0 to 300 tokens at 0 to 2500, G = 6, 4 kv heads, 196 us.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -49,8 +67,8 @@ constexpr int kThreads = 384;  // three warpgroups
 // Registers per thread after setmaxnreg: the launch has 65536 / 384 = 168 a
 // thread, and the split must not add up to more (the host checks the compiled
 // count before the first launch).
-constexpr int kSoftmaxRegs = 216;
-constexpr int kOtherRegs = 72;
+constexpr int kSoftmaxRegs = 208;
+constexpr int kOtherRegs = 88;
 constexpr int kLaunchRegs = 168;
 static_assert(2 * kSoftmaxRegs + kOtherRegs <= 3 * kLaunchRegs, "register split exceeds the launch allocation");
 constexpr int kWarpLoad = 8;
@@ -62,8 +80,28 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kKStages = 3;    // K ring (e4m3, 16 KB a tile)
 constexpr int kVRaw = 2;       // V copy ring (e4m3, 16 KB a tile)
 constexpr int kVStages = 2;    // V ring in f16 (32 KB a tile)
+constexpr int kPieces = 4;     // pieces known ahead
+constexpr int kBad = 8;        // key iterations whose bad-block bits are kept (the K ring is 3 ahead)
+// Length of a unit on the line beyond its keys: a piece's start and end take
+// about as long as three key tiles.
+constexpr int kUnitCost = 3 * kBN;
+constexpr int kMinStretch = 4 * kBN;  // about a piece's start and end
+constexpr int kMinCutTiles = 16;  // shorter units are not worth a cut (cut_units)
+constexpr int kRows = 2 * kBM;                  // rows of a unit
 constexpr uint32_t kTile8 = kBN * kD;           // bytes of an e4m3 tile
 constexpr uint32_t kChunkBytes = kBM * 128;     // 128 rows x 128 bytes
+
+// A piece of a unit, as the copy warp hands it to the others.
+struct Piece {
+  int more;              // 0: no piece, the stretch is done
+  int n[2];              // key tiles of this piece that query tile 0 / 1 sees
+  int j0;                // first key tile
+  int b, hk;
+  int qoff, T, S;        // of the sequence
+  int tok0;              // first token of the unit
+  int whole;             // the whole unit
+  int slot;              // of a cut unit's piece in the workspace
+};
 
 struct __align__(1024) Smem {
   // q: two 64-column chunks of bf16 as copied; then the hi tile in chunk 0
@@ -72,28 +110,45 @@ struct __align__(1024) Smem {
   uint8_t k[kKStages][kTile8];
   uint8_t v_raw[kVRaw][kTile8];
   uint8_t v[kVStages][2][kChunkBytes];  // f16, two 64-column chunks
-  uint64_t q_full[2], q_ready[2];
+  uint8_t stage[8][2048];               // output of a softmax warp, 64 bytes of each row at a time
+  uint64_t q_full[2], q_ready[2], q_free[2];
   uint64_t k_full[kKStages];
   // kv_done[i % kKStages] completes when key iteration i has finished with
   // K(i) and V(i - 1)
   uint64_t kv_done[kKStages];
   uint64_t vr_full[kVRaw], vr_empty[kVRaw];
   uint64_t v_full[kVStages];
-  uint64_t s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t piece_full[kPieces], piece_free[kPieces];
   uint64_t mma_done;
+  Piece piece[kPieces];
   int v_valid[kVRaw];      // keys of the raw tile inside the sequence
   uint32_t v_bad[kVRaw];   // its blocks outside the pool
+  uint32_t bad[kBad];      // the same of key iteration i at i % kBad, for the softmax
+  long long begin, end, stretch;  // this CTA's stretch of the line
+  int index;                      // its place among the stretches
+  int unit_keys;                  // length of every unit on the line; 0: its keys and kUnitCost
+  int b0, mb0;                    // the sequence and query block that it begins in
+  long long rest;                 // where in them (kv heads one behind the other)
   uint32_t tmem_base;
   int abort_flag;
 };
 
 constexpr size_t smem_bytes() { return sizeof(Smem); }
 
+// A cut unit, written for the stretch that holds its last piece.
+struct Cut {
+  int c0;                // stretch of its first piece, -1: this one ends no cut unit
+  int hk, qoff, tok0, T;
+};
+
 struct Params {
   __nv_bfloat16* o;            // [total_q, Hq, 128]
   float* lse;                  // [Hq, total_q] or null
-  float* part_o;               // [splits, total_q, Hq, 128] when splits > 1
-  float* part_lse;             // [splits, total_q, Hq]
+  float* part_o;               // [slots][256][128]: pieces of cut units
+  float* part_lse;             // [slots][256]
+  Cut* cuts;                   // [num_cuts], a stretch each
+  int num_cuts;
   const int32_t* cu_q;         // [B + 1]
   const int32_t* block_table;  // [B, max_blocks]
   const int32_t* seq_lens;     // [B]
@@ -102,9 +157,12 @@ struct Params {
   int tok_tile;                // tokens of a query tile: 128 / G
   int g_magic;                 // ceil(2^16 / G): r / G = r * g_magic >> 16 for r < 128
   int total_q, causal;
-  int num_mblocks;             // ceil(max_seqlen_q / (2 tok_tile))
-  int items;                   // B <= 32: query blocks at most; 0: B * num_mblocks of them
-  int splits, chunk;           // ranges of `chunk` key tiles
+  int slots;                   // workspace slots of a stretch: 2, or 1 when it is one piece
+  // keys of a stretch, with every unit unit_keys long; 0: the kernel decides
+  // between a unit a CTA (unit_keys each) and num_cuts equal stretches
+  long long stretch;
+  int unit_keys;
+  int sms;
   float scale_log2;            // scale * k_scale * log2(e)
   float v_scale;
 };
@@ -152,6 +210,13 @@ __device__ __forceinline__ void split_e4m3(const uint32_t (&w)[8], float up, uin
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
+// threadIdx.x, read anew: the compiler does not keep what is derived from it.
+__device__ __forceinline__ int thread_index() {
+  int x;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(x));
+  return x;
+}
+
 // Key tiles that the tokens [t0, t0 + n) of a sequence see.
 __device__ __forceinline__ int key_tiles(int t0, int n, int T, int S, int causal) {
   if (t0 >= T) return 0;
@@ -161,27 +226,75 @@ __device__ __forceinline__ int key_tiles(int t0, int n, int T, int S, int causal
   return kmax < 0 ? 0 : kmax / kBN + 1;
 }
 
+// One sequence on the line: nb units of `heads` pieces each, unit mb as long as
+// fixed + min(T, (mb + 1) step) when step > 0, else fixed.
+struct Line {
+  int qoff, T, S, nb, step;
+  long long fixed;
+
+  __device__ __forceinline__ Line(const Params& p, int unit_keys, int b) {
+    qoff = __ldg(p.cu_q + b);
+    T = max(__ldg(p.cu_q + b + 1) - qoff, 0);
+    S = min(max(__ldg(p.seq_lens + b), 0), p.max_blocks * 16);
+    const int rows = 2 * p.tok_tile;  // tokens of a unit
+    nb = (T + rows - 1) / rows;
+    step = 0;
+    fixed = unit_keys;
+    if (unit_keys == 0) {
+      step = p.causal ? rows : 0;
+      fixed = kUnitCost + (p.causal ? max(S - T, 0) : S);
+    }
+  }
+  __device__ __forceinline__ long long unit(int mb) const {
+    return fixed + (step > 0 ? min(static_cast<long long>(T), static_cast<long long>(mb + 1) * step) : 0);
+  }
+  __device__ __forceinline__ long long before(int mb) const {  // units 0 .. mb - 1, mb <= nb
+    long long x = mb * fixed;
+    if (step > 0) {
+      const long long full = mb < nb ? mb : nb - 1;  // units with all their tokens
+      x += step * (full * (full + 1) / 2) + (mb == nb && nb > 0 ? T : 0);
+    }
+    return x;
+  }
+};
+
+// Whether the line is cut into even stretches, or every CTA takes a unit.
+// A unit a CTA, handed out as CTAs end, leaves SMs idle while the last ones run:
+// for units of one length L it is L (ceil(u) - u) key tiles with u units an SM;
+// other lengths fill in, the more the larger u is.  Cutting costs the pieces'
+// workspace, their merge, and one more start and end an SM, which together took
+// as long as 15 to 30 key tiles.  Measured with 8 kv heads, G = 4, a unit a CTA /
+// cut: 2048 tokens at 32k (u = 1.7, L = 248) 1000 / 906 us; 2 x 2048 at 8k to 24k
+// (1.7, 125) 937 / 865; 6 x 512 at 1k to 8k (2.6, 35) 259 / 253; 4 x 512 at 1k to
+// 8k (1.7, 35) 149 / 174; 8 x 512 at .5k to 7.7k (3.3, 24) 239 / 276.
+__device__ __forceinline__ bool cut_units(long long keys, long long units, int sms) {
+  if (units == 0) return false;
+  const float len = static_cast<float>(keys) / static_cast<float>(units) - kUnitCost;
+  const long long waves = (units + sms - 1) / sms;
+  const float idle = len / kBN * (static_cast<float>(waves) - static_cast<float>(units) / static_cast<float>(sms));
+  return idle > (waves > 1 ? 32.f : 16.f);
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_fp8_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const Params p) {
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
   // Used as it is: an address computed from it would lose its state space, and
   // every access would be a generic one with a 64-bit address.
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  // blockIdx.x = (item, range, kv head), the kv head fastest
-  const int hk = static_cast<int>(blockIdx.x) % p.Hkv;
-  const int split = (static_cast<int>(blockIdx.x) / p.Hkv) % p.splits;
-  const int item = static_cast<int>(blockIdx.x) / p.Hkv / p.splits;
+  const int cta = blockIdx.x;
 
   if (warp == kWarpLoad && lane == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sm.q_full[t], 1);
       mbar_init(&sm.q_ready[t], 4);
+      mbar_init(&sm.q_free[t], 1);
       mbar_init(&sm.s_full[t], 1);
       mbar_init(&sm.p_full[t], 4);
       mbar_init(&sm.o_full[t], 1);
+      mbar_init(&sm.o_free[t], 4);
     }
     for (int s = 0; s < kKStages; ++s) {
       mbar_init(&sm.k_full[s], 1);
@@ -192,6 +305,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.vr_empty[s], kConvWarps);
     }
     for (int s = 0; s < kVStages; ++s) mbar_init(&sm.v_full[s], kConvWarps);
+    for (int i = 0; i < kPieces; ++i) {
+      mbar_init(&sm.piece_full[i], 1);
+      mbar_init(&sm.piece_free[i], 8 + 1 + kConvWarps);
+    }
     mbar_init(&sm.mma_done, 1);
     sm.abort_flag = 0;
     fence_mbarrier_init();
@@ -199,68 +316,89 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
-  grid_dependency_wait();
-  grid_launch_dependents();
-
-  // CTA -> (sequence b, query block mb).  Compact grid (B <= 32): lane i
-  // holds sequence i's count of query blocks; sequence-major, top block first,
-  // so that a sequence's blocks run together and share its keys in L2.
-  const int rows_cta = 2 * p.tok_tile;  // tokens of a CTA
-  int b, mb;
-  if (p.items > 0) {
-    const int len = lane < p.B ? p.cu_q[lane + 1] - p.cu_q[lane] : 0;
-    const int nblocks = len > 0 ? (len + rows_cta - 1) / rows_cta : 0;
-    int incl = nblocks;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const int excl = incl - nblocks;
-    const uint32_t m = __ballot_sync(0xffffffffu, item >= excl && item < incl);
-    if (m == 0) return;  // past the last item (the grid is an upper bound)
-    b = __ffs(m) - 1;
-    mb = __shfl_sync(0xffffffffu, nblocks, b) - 1 - (item - __shfl_sync(0xffffffffu, excl, b));
-  } else {
-    mb = p.num_mblocks - 1 - item / p.B;
-    b = item % p.B;
-  }
-  const int qoff = p.cu_q[b];
-  const int T = p.cu_q[b + 1] - qoff;
-  int S = p.seq_lens[b];
-  if (S < 0 || S > p.max_blocks * 16) {
-    if (threadIdx.x == 0 && hk == 0 && split == 0) atomicOr(&g_devstatus, kDevStatusBadSeqLen);
-    S = S < 0 ? 0 : p.max_blocks * 16;
-  }
-  const int tok0 = mb * rows_cta;
-  if (tok0 >= T) return;  // a query block past the sequence (uniform over the CTA)
-  const int j0 = split * p.chunk;  // first key tile of this range
-  const int n0 = min(max(key_tiles(tok0, p.tok_tile, T, S, p.causal) - j0, 0), p.chunk);
-  const int n1 = min(max(key_tiles(tok0 + p.tok_tile, p.tok_tile, T, S, p.causal) - j0, 0), p.chunk);
-  const int n_max = max(n0, n1);
-  if (n_max == 0 && p.splits > 1) {
-    // nothing of this range is seen: the merge skips it
-    for (int i = threadIdx.x; i < 2 * p.tok_tile * p.G; i += kThreads) {
-      const int tok = tok0 + i / p.G;
-      if (tok < T && qoff + tok < p.total_q)
-        p.part_lse[(static_cast<size_t>(split) * p.total_q + qoff + tok) * p.Hq + hk * p.G + i % p.G] = -INFINITY;
-    }
-    return;
-  }
   if (warp == 0) {
     tmem_alloc(&sm.tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  const int lead = (n1 >= n0 && n1 > 0) ? 1 : 0;  // the tile with more key tiles goes first
-  const int tile_rows = p.tok_tile * p.G;
-  if (warp == kWarpLoad && lane == 0) {
-    const int nt[2] = {n0, n1};
-    for (int i = 0; i < 2; ++i) {
-      const int t = i == 0 ? lead : 1 - lead;
-      if (nt[t] == 0) continue;
-      mbar_arrive_expect_tx(&sm.q_full[t], static_cast<uint32_t>(tile_rows) * kD * 2);
-      for (int c = 0; c < 2; ++c)
-        tma_load_3d(sm.q[t][c], &tmQ, &sm.q_full[t], c * 64, hk * p.G, qoff + tok0 + t * p.tok_tile);
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  if (warp == kWarpMma) {
+    // the line's length, this CTA's stretch of it, and where that begins
+    long long keys = 0, units = 0;
+    for (int b = lane; b < p.B; b += 32) {
+      const int raw = __ldg(p.seq_lens + b);
+      if (cta == 0 && (raw < 0 || raw > p.max_blocks * 16)) atomicOr(&g_devstatus, kDevStatusBadSeqLen);
+      const Line line(p, 0, b);
+      keys += line.before(line.nb);
+      units += line.nb;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      keys += __shfl_xor_sync(0xffffffffu, keys, o);
+      units += __shfl_xor_sync(0xffffffffu, units, o);
+    }
+    keys *= p.Hkv;
+    units *= p.Hkv;
+    long long total = units * p.unit_keys, stretch = p.stretch;
+    int unit_keys = p.unit_keys;
+    if (stretch == 0) {
+      stretch = unit_keys;
+      if (cut_units(keys, units, p.sms)) {
+        unit_keys = 0;
+        total = keys;
+        stretch = (total + p.num_cuts - 1) / p.num_cuts;
+        if (stretch < kMinStretch) stretch = kMinStretch;
+      }
+    }
+    // The last stretch first: with causal masks the units of a sequence grow.
+    const long long count = min((total + stretch - 1) / stretch, static_cast<long long>(gridDim.x));
+    const int index = cta < count ? static_cast<int>(count) - 1 - cta : cta;
+    const long long begin = stretch * index;
+    long long before = 0, rest = 0;
+    int b0 = p.B, mb0 = 0;
+    for (int base = 0; base < p.B && b0 == p.B; base += 32) {
+      const int b = base + lane;
+      long long len = 0;
+      if (b < p.B) {
+        const Line line(p, unit_keys, b);
+        len = line.before(line.nb) * p.Hkv;
+      }
+      long long incl = len;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, begin < before + incl);
+      if (m != 0) {
+        const int w = __ffs(m) - 1;
+        b0 = base + w;
+        rest = begin - before - __shfl_sync(0xffffffffu, incl - len, w);
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (b0 < p.B) {  // the last query block that begins at or before `rest`
+      const Line line(p, unit_keys, b0);
+      int hi = line.nb;
+      while (hi - mb0 > 1) {
+        const int mid = (mb0 + hi) / 2;
+        if (line.before(mid) * p.Hkv <= rest)
+          mb0 = mid;
+        else
+          hi = mid;
+      }
+      rest -= line.before(mb0) * p.Hkv;
+    }
+    if (lane == 0) {
+      sm.begin = begin;
+      sm.end = min(begin + stretch, total);
+      sm.stretch = stretch;
+      sm.index = index;
+      sm.unit_keys = unit_keys;
+      sm.b0 = b0;
+      sm.mb0 = mb0;
+      sm.rest = rest;
     }
   }
   tc_fence_before();
@@ -268,113 +406,236 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
   volatile int* abort_flag = &sm.abort_flag;
+  const int tile_rows = p.tok_tile * p.G;
+  auto wait_piece = [&](int i) -> bool {
+    return mbar_wait(&sm.piece_full[i % kPieces], (i / kPieces) & 1, abort_flag);
+  };
 
   if (warp >= 8) {
     reg_dealloc<kOtherRegs>();
     if (warp == kWarpLoad) {
       // ------------------------------ copies ------------------------------
-      // Lane L < 8 issues K's copy of block L of the tile, lane 8 + L V's.
-      int k_issued = 0, v_issued = 0;
+      // Walks the stretch for the whole CTA.  Lane L < 8 issues K's copy of
+      // block L of the tile, lane 8 + L V's.
+      long long pos = sm.begin, lo = 0;
+      const long long end = sm.end;
+      int b = sm.b0, mb = sm.mb0, hk = 0;
+      // The unit's first places hold no key: an end of a stretch among them
+      // counts as the unit's beginning, so that no piece is without a key.
+      const int unit_keys = sm.unit_keys, index = sm.index;
+      const int cost = unit_keys > 0 ? 0 : kUnitCost;
+      if (b < p.B) {
+        const long long u = Line(p, unit_keys, b).unit(mb);
+        hk = static_cast<int>(sm.rest / u);
+        lo = sm.rest - hk * u;
+        if (lo <= cost) pos -= lo, lo = 0;
+      }
+      if (lane == 0 && index < p.num_cuts) p.cuts[index].c0 = -1;
+      int jt = 0;                // key iterations, over all pieces
+      int part0 = 0, part1 = 0;  // pieces that query tile 0 / 1 has taken part in
       const int il = lane & 7;
       const uint64_t kv_pol = l2_policy_evict_last();
       bool ok = true;
-      for (int j = 0; j < n_max; ++j) {
-        const int s = j % kKStages, sv = j % kVRaw;
-        const int key0 = (j0 + j) * kBN;
-        const int valid = min(kBN, S - key0);
-        const int nblk = (valid + 15) / 16;
-        const int id = il < nblk ? __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + key0 / 16 + il) : 0;
-        const uint32_t bad =
-            __ballot_sync(0xffffffffu, lane < nblk && static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks));
-        if (bad && lane == 0) atomicOr(&g_devstatus, kDevStatusBadBlock);
-        const bool my_copy = il < nblk && !((bad >> il) & 1u);
-        const uint32_t bytes = static_cast<uint32_t>(nblk - __popc(bad)) * 16 * kD;
-        if (lane == 0) {
-          ok = mbar_wait(&sm.kv_done[s], ((j / kKStages) & 1) ^ 1, abort_flag);  // iteration j - kKStages freed it
-          if (ok) mbar_arrive_expect_tx(&sm.k_full[s], bytes);
+      for (int i = 0; ok; ++i) {
+        while (b < p.B && Line(p, unit_keys, b).nb == 0) ++b;
+        bool more = pos < end && b < p.B;
+        if (more) {
+          const long long u = Line(p, unit_keys, b).unit(mb), hi = min(u, lo + (end - pos));
+          if (hi < u && hi <= cost) more = false;
         }
-        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-        if (lane < 8 && my_copy)
-          tma_load_2d_hint(sm.k[s] + il * 16 * 128, &tmK, &sm.k_full[s], hk * kD, id * 16, kv_pol);
-        if (lane == 0) {
-          k_issued = j + 1;
-          ok = mbar_wait(&sm.vr_empty[sv], ((j / kVRaw) & 1) ^ 1, abort_flag);
-          if (ok) {
-            sm.v_valid[sv] = valid;
-            sm.v_bad[sv] = bad;
-            mbar_arrive_expect_tx(&sm.vr_full[sv], bytes);
+        Piece pc;
+        pc.more = more;
+        int n_max = 0;
+        if (more) {
+          const Line line(p, unit_keys, b);
+          const long long u = line.unit(mb);
+          const long long hi = min(u, lo + (end - pos));
+          const int t0 = static_cast<int>((max(lo - cost, 0LL) + kBN - 1) / kBN);
+          const int t1 = static_cast<int>(min((max(hi - cost, 0LL) + kBN - 1) / kBN, 0x7fffffffLL / kBN));
+          pc.tok0 = mb * 2 * p.tok_tile;
+          pc.n[0] = max(min(key_tiles(pc.tok0, p.tok_tile, line.T, line.S, p.causal), t1) - t0, 0);
+          pc.n[1] = max(min(key_tiles(pc.tok0 + p.tok_tile, p.tok_tile, line.T, line.S, p.causal), t1) - t0, 0);
+          pc.j0 = t0;
+          pc.b = b;
+          pc.hk = hk;
+          pc.qoff = line.qoff;
+          pc.T = line.T;
+          pc.S = line.S;
+          pc.whole = lo == 0 && hi == u;
+          const bool last = hi == u;
+          pc.slot = p.slots * index + (p.slots > 1 && !last ? 1 : 0);
+          n_max = max(pc.n[0], pc.n[1]);
+          if (last && !pc.whole && lane == 0) {
+            Cut& c = p.cuts[index];
+            c.c0 = static_cast<int>((pos - lo + cost) / sm.stretch);
+            c.hk = hk;
+            c.qoff = line.qoff;
+            c.tok0 = pc.tok0;
+            c.T = line.T;
+          }
+          pos += hi - lo;
+          lo = 0;
+          if (++hk == p.Hkv) {
+            hk = 0;
+            if (++mb == line.nb) mb = 0, ++b;
           }
         }
-        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-        if (lane >= 8 && lane < 16 && my_copy)
-          tma_load_2d_hint(sm.v_raw[sv] + il * 16 * 128, &tmV, &sm.vr_full[sv], hk * kD, id * 16, kv_pol);
-        v_issued = j + 1;
+        if (lane == 0) {
+          ok = mbar_wait(&sm.piece_free[i % kPieces], ((i / kPieces) & 1) ^ 1, abort_flag);
+          if (ok) {
+            sm.piece[i % kPieces] = pc;
+            mbar_arrive(&sm.piece_full[i % kPieces]);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok || !more) break;
+        if (n_max == 0) continue;
+        if (lane == 0) {
+          const int lead = (pc.n[1] >= pc.n[0] && pc.n[1] > 0) ? 1 : 0;
+          for (int e = 0; e < 2 && ok; ++e) {
+            const int t = e == 0 ? lead : 1 - lead;
+            if ((t ? pc.n[1] : pc.n[0]) == 0) continue;
+            // the piece before has read it
+            ok = mbar_wait(&sm.q_free[t], ((t ? part1 : part0) & 1) ^ 1, abort_flag);
+            if (!ok) break;
+            mbar_arrive_expect_tx(&sm.q_full[t], static_cast<uint32_t>(tile_rows) * kD * 2);
+            for (int c = 0; c < 2; ++c)
+              tma_load_3d(sm.q[t][c], &tmQ, &sm.q_full[t], c * 64, pc.hk * p.G, pc.qoff + pc.tok0 + t * p.tok_tile);
+            (t ? part1 : part0) += 1;
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        const int32_t* table = p.block_table + static_cast<size_t>(pc.b) * p.max_blocks;
+        const int nblk_all = (pc.S + 15) / 16;
+        int id_next = pc.j0 * 8 + il < nblk_all ? __ldg(table + pc.j0 * 8 + il) : 0;
+        for (int j = 0; j < n_max && ok; ++j, ++jt) {
+          const int s = jt % kKStages, sv = jt % kVRaw;
+          const int blk0 = (pc.j0 + j) * 8;
+          const int valid = min(kBN, pc.S - blk0 * 16);
+          const int nblk = (valid + 15) / 16;
+          const int id = id_next;
+          if (j + 1 < n_max) id_next = blk0 + 8 + il < nblk_all ? __ldg(table + blk0 + 8 + il) : 0;
+          const uint32_t bad = __ballot_sync(
+              0xffffffffu, lane < nblk && static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks));
+          if (bad && lane == 0) atomicOr(&g_devstatus, kDevStatusBadBlock);
+          const bool my_copy = il < nblk && !((bad >> il) & 1u);
+          const uint32_t bytes = static_cast<uint32_t>(nblk - __popc(bad)) * 16 * kD;
+          if (lane == 0) {
+            ok = mbar_wait(&sm.kv_done[s], ((jt / kKStages) & 1) ^ 1, abort_flag);  // iteration jt - kKStages
+            if (ok) {
+              sm.bad[jt % kBad] = bad;
+              mbar_arrive_expect_tx(&sm.k_full[s], bytes);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          if (lane < 8 && my_copy)
+            tma_load_2d_hint(sm.k[s] + il * 16 * 128, &tmK, &sm.k_full[s], pc.hk * kD, id * 16, kv_pol);
+          if (lane == 0) {
+            ok = mbar_wait(&sm.vr_empty[sv], ((jt / kVRaw) & 1) ^ 1, abort_flag);
+            if (ok) {
+              sm.v_valid[sv] = valid;
+              sm.v_bad[sv] = bad;
+              mbar_arrive_expect_tx(&sm.vr_full[sv], bytes);
+            } else {
+              mbar_wait_drain(&sm.k_full[s], (jt / kKStages) & 1);  // the K copy just issued
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          if (lane >= 8 && lane < 16 && my_copy)
+            tma_load_2d_hint(sm.v_raw[sv] + il * 16 * 128, &tmV, &sm.vr_full[sv], pc.hk * kD, id * 16, kv_pol);
+        }
       }
       if (lane == 0 && *abort_flag) {
         // let the copies already issued land before shared memory is released
-        if (n0 > 0) mbar_wait_drain(&sm.q_full[0], 0);
-        if (n1 > 0) mbar_wait_drain(&sm.q_full[1], 0);
-        for (int j = max(0, k_issued - kKStages); j < k_issued; ++j)
-          mbar_wait_drain(&sm.k_full[j % kKStages], (j / kKStages) & 1);
-        for (int j = max(0, v_issued - kVRaw); j < v_issued; ++j)
-          mbar_wait_drain(&sm.vr_full[j % kVRaw], (j / kVRaw) & 1);
+        if (part0 > 0) mbar_wait_drain(&sm.q_full[0], (part0 - 1) & 1);
+        if (part1 > 0) mbar_wait_drain(&sm.q_full[1], (part1 - 1) & 1);
+        for (int j = max(0, jt - kKStages); j < jt; ++j) mbar_wait_drain(&sm.k_full[j % kKStages], (j / kKStages) & 1);
+        for (int j = max(0, jt - kVRaw); j < jt; ++j) mbar_wait_drain(&sm.vr_full[j % kVRaw], (j / kVRaw) & 1);
       }
     } else if (warp == kWarpMma) {
       // ---------------------------- MMA issuer ----------------------------
       if (lane == 0) {
         constexpr uint32_t idesc_qk = make_idesc_fmt0(kBM, kBN, 0, 0);  // e4m3, both K-major
         constexpr uint32_t idesc_pv = make_idesc_fmt0(kBM, kD, 0, 1);   // f16, P (TMEM), V MN-major
-        const int nt[2] = {n0, n1};
-        const int ord[2] = {lead, 1 - lead};
+        constexpr uint32_t kHi = make_sdesc_hi_sw128(1024);
+        const uint32_t q_lo = make_sdesc_lo(smem_u32(sm.q), 16), k_lo = make_sdesc_lo(smem_u32(sm.k), 16);
+        const uint32_t v_lo = make_sdesc_lo(smem_u32(sm.v), kChunkBytes);
         bool ok = true;
-        auto issue_pv = [&](int t, int jj, bool wait_v, bool last) -> bool {
-          const int s = jj % kVStages;
-          if (wait_v && !mbar_wait(&sm.v_full[s], (jj / kVStages) & 1, abort_flag)) return false;
-          const uint32_t tS = tmem + t * kBN;
-          const uint32_t tO = tmem + 2 * kBN + t * kD;
-          const uint32_t vbase = smem_u32(sm.v[s][0]);
-          if (!mbar_wait(&sm.p_full[t], jj & 1, abort_flag)) return false;
-          tc_fence_after();
+        int jt = 0;             // key iterations, over all pieces
+        int ks = 0;             // K ring: slot and parity of iteration jt
+        uint32_t kph = 0;
+        // of query tile 0 / 1, over all pieces (scalars: an array indexed by the
+        // tile would live in local memory)
+        int seen0 = 0, seen1 = 0;  // key tiles
+        int part0 = 0, part1 = 0;  // pieces that it has taken part in
+        for (int i = 0; ok; ++i) {
+          if (!(ok = wait_piece(i))) break;
+          const Piece& pc = sm.piece[i % kPieces];
+          const int more = pc.more;
+          const int n0 = more ? pc.n[0] : 0, n1 = more ? pc.n[1] : 0;
+          mbar_arrive(&sm.piece_free[i % kPieces]);
+          if (!more) break;
+          const int n_max = max(n0, n1);
+          if (n_max == 0) continue;
+          const int lead = (n1 >= n0 && n1 > 0) ? 1 : 0;  // the tile with more key tiles goes first
+          const int jt0 = jt;
+          auto tiles = [&](int t) { return t ? n1 : n0; };
+          auto seen = [&](int t) { return t ? seen1 : seen0; };
+          auto part = [&](int t) { return t ? part1 : part0; };
+          auto issue_pv = [&](int t, int jj, bool wait_v, bool last) -> bool {
+            const int s = (jt0 + jj) % kVStages;
+            if (wait_v && !mbar_wait(&sm.v_full[s], ((jt0 + jj) / kVStages) & 1, abort_flag)) return false;
+            const uint32_t tS = tmem + t * kBN;
+            const uint32_t tO = tmem + 2 * kBN + t * kD;
+            if (!mbar_wait(&sm.p_full[t], (seen(t) + jj) & 1, abort_flag)) return false;
+            // the output of the piece before has been read
+            if (jj == 0 && !mbar_wait(&sm.o_free[t], (part(t) & 1) ^ 1, abort_flag)) return false;
+            tc_fence_after();
 #pragma unroll
-          for (int kk = 0; kk < kBN / 16; ++kk) {
-            const uint64_t bdesc = make_sdesc_sw128(vbase + kk * 16 * 128, kChunkBytes, 1024);
-            umma_ts(tO, tS + kk * 8, bdesc, idesc_pv, (jj > 0 || kk > 0) ? 1u : 0u);
-          }
-          if (last) umma_commit(&sm.o_full[t]);
-          return true;
-        };
-        for (int j = 0; j < n_max && ok; ++j) {
-          const int s = j % kKStages;
-          if (!(ok = mbar_wait(&sm.k_full[s], (j / kKStages) & 1, abort_flag))) break;
-          tc_fence_after();
-          for (int i = 0; i < 2 && ok; ++i) {
-            const int t = ord[i];
-            // the previous P_t must be consumed before S_t is overwritten
-            if (j >= 1 && j - 1 < nt[t]) ok = issue_pv(t, j - 1, i == 0, j == nt[t]);
-            if (ok && j == 0 && nt[t] > 0) {
-              ok = mbar_wait(&sm.q_ready[t], 0, abort_flag);
-              tc_fence_after();
+            for (int kk = 0; kk < kBN / 16; ++kk) {
+              umma_ts_words<kHi>(tO, tS + kk * 8, v_lo + s * (2 * kChunkBytes >> 4) + kk * (16 * 128 >> 4), idesc_pv,
+                                 kk > 0 ? 1u : (jj > 0 ? 1u : 0u));
             }
-            if (ok && j < nt[t]) {
-              const uint32_t tS = tmem + t * kBN;
-              const uint32_t qbase = smem_u32(sm.q[t][0]);
-              const uint32_t kbase = smem_u32(sm.k[s]);
+            if (last) umma_commit(&sm.o_full[t]);
+            return true;
+          };
+          for (int j = 0; j < n_max && ok; ++j) {
+            if (!(ok = mbar_wait(&sm.k_full[ks], kph, abort_flag))) break;
+            tc_fence_after();
 #pragma unroll
-              for (int kk = 0; kk < 8; ++kk) {  // hi, then lo; 32 of the head dim at a time
-                const uint64_t adesc = make_sdesc_sw128(qbase + (kk / 4) * kChunkBytes + (kk % 4) * 32, 16, 1024);
-                const uint64_t bdesc = make_sdesc_sw128(kbase + (kk % 4) * 32, 16, 1024);
-                umma_ss_f8(tS, adesc, bdesc, idesc_qk, kk > 0 ? 1u : 0u);
+            for (int e = 0; e < 2; ++e) {
+              const int t = e == 0 ? lead : 1 - lead;
+              const int nt = tiles(t);
+              // the previous P_t must be consumed before S_t is overwritten
+              if (ok && j >= 1 && j - 1 < nt) ok = issue_pv(t, j - 1, e == 0, j == nt);
+              if (ok && j == 0 && nt > 0) {
+                ok = mbar_wait(&sm.q_ready[t], part(t) & 1, abort_flag);
+                tc_fence_after();
               }
-              umma_commit(&sm.s_full[t]);
+              if (ok && j < nt) {
+                const uint32_t tS = tmem + t * kBN;
+                const uint32_t a_lo = q_lo + t * (2 * kChunkBytes >> 4), b_lo = k_lo + ks * (kTile8 >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)  // hi, then lo; 32 of the head dim at a time
+                  umma_ss_f8_words<kHi>(tS, a_lo + (kk / 4) * (kChunkBytes >> 4) + (kk % 4) * 2, b_lo + (kk % 4) * 2,
+                                        idesc_qk, kk > 0 ? 1u : 0u);
+                umma_commit(&sm.s_full[t]);
+                if (j == nt - 1) umma_commit(&sm.q_free[t]);
+              }
             }
+            if (!ok) break;
+            umma_commit(&sm.kv_done[ks]);  // K(j) and V(j - 1) are free
+            if (++ks == kKStages) ks = 0, kph ^= 1;
           }
-          if (!ok) break;
-          umma_commit(&sm.kv_done[s]);  // K(j) and V(j - 1) are free
-        }
-        if (ok && n_max > 0) {
-          const int jl = n_max - 1;
-          for (int i = 0; i < 2 && ok; ++i)
-            if (jl < nt[ord[i]]) ok = issue_pv(ord[i], jl, i == 0, true);
+          if (ok) ok = issue_pv(lead, n_max - 1, true, true);
+          if (ok && tiles(1 - lead) == n_max) ok = issue_pv(1 - lead, n_max - 1, false, true);
+          jt += n_max;
+          seen0 += n0;
+          seen1 += n1;
+          part0 += n0 > 0;
+          part1 += n1 > 0;
         }
         umma_commit(&sm.mma_done);
         mbar_wait_drain(&sm.mma_done, 0);
@@ -391,261 +652,297 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int dst_a = c * static_cast<int>(kChunkBytes) + x * 128 + (((2 * (u & 3) + c) ^ x) << 4);
       const int dst_b = c * static_cast<int>(kChunkBytes) + x * 128 + (((2 * (u & 3) + 1 - c) ^ x) << 4);
       bool ok = true;
-      for (int j = 0; j < n_max; ++j) {
-        const int sr = j % kVRaw, s = j % kVStages;
-        ok = __all_sync(0xffffffffu, mbar_wait(&sm.vr_full[sr], (j / kVRaw) & 1, abort_flag));
+      int jt = 0;  // key iterations, over all pieces
+      for (int i = 0; ok; ++i) {
+        ok = __all_sync(0xffffffffu, wait_piece(i));
         if (!ok) break;
-        if (j >= kVStages) {  // V(j - kVStages) was freed by iteration j - kVStages + 1
-          const int it = j - kVStages + 1;
-          ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_done[it % kKStages], (it / kKStages) & 1, abort_flag));
-          if (!ok) break;
-        }
-        uint8_t* src = sm.v_raw[sr] + src_off;
-        uint8_t* dst = sm.v[s][0];
-        const int valid = sm.v_valid[sr];
-        const uint32_t bad = sm.v_bad[sr];
-        if (valid < kBN || bad != 0) {  // each lane clears the codes that it reads below
-          for (int i = 0; i < kBN / 8; ++i)
-            if (i * 8 + x >= valid || ((bad >> (i >> 1)) & 1u))
-              *reinterpret_cast<uint4*>(src + i * 1024) = make_uint4(0u, 0u, 0u, 0u);
-        }
-#pragma unroll
-        for (int part = 0; part < kBN / 32; ++part) {
-          uint4 raw[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) raw[i] = *reinterpret_cast<const uint4*>(src + (part * 4 + i) * 1024);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t a0 = c ? raw[i].z : raw[i].x, a1 = c ? raw[i].w : raw[i].y;
-            const uint32_t b0 = c ? raw[i].x : raw[i].z, b1 = c ? raw[i].y : raw[i].w;
-            *reinterpret_cast<uint4*>(dst + dst_a + (part * 4 + i) * 1024) =
-                make_uint4(e4m3x2_to_f16x2(a0 & 0xffffu), e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(a1 & 0xffffu),
-                           e4m3x2_to_f16x2(a1 >> 16));
-            *reinterpret_cast<uint4*>(dst + dst_b + (part * 4 + i) * 1024) =
-                make_uint4(e4m3x2_to_f16x2(b0 & 0xffffu), e4m3x2_to_f16x2(b0 >> 16), e4m3x2_to_f16x2(b1 & 0xffffu),
-                           e4m3x2_to_f16x2(b1 >> 16));
-          }
-        }
-        fence_proxy_async_smem();  // the generic writes before the tensor core reads the tile
+        const int more = sm.piece[i % kPieces].more;
+        const int n_max = more ? max(sm.piece[i % kPieces].n[0], sm.piece[i % kPieces].n[1]) : 0;
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.vr_empty[sr]);
-          mbar_arrive(&sm.v_full[s]);
+        if (lane == 0) mbar_arrive(&sm.piece_free[i % kPieces]);
+        if (!more) break;
+        for (int j = 0; j < n_max && ok; ++j, ++jt) {
+          const int sr = jt % kVRaw, s = jt % kVStages;
+          ok = __all_sync(0xffffffffu, mbar_wait(&sm.vr_full[sr], (jt / kVRaw) & 1, abort_flag));
+          if (!ok) break;
+          if (jt >= kVStages) {  // V(jt - kVStages) was freed by iteration jt - kVStages + 1
+            const int it = jt - kVStages + 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(&sm.kv_done[it % kKStages], (it / kKStages) & 1, abort_flag));
+            if (!ok) break;
+          }
+          uint8_t* src = sm.v_raw[sr] + src_off;
+          uint8_t* dst = sm.v[s][0];
+          const int valid = sm.v_valid[sr];
+          const uint32_t bad = sm.v_bad[sr];
+          if (valid < kBN || bad != 0) {  // each lane clears the codes that it reads below
+            for (int i = 0; i < kBN / 8; ++i)
+              if (i * 8 + x >= valid || ((bad >> (i >> 1)) & 1u))
+                *reinterpret_cast<uint4*>(src + i * 1024) = make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll 1
+          for (int part = 0; part < kBN / 32; ++part) {
+            uint4 raw[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) raw[i] = *reinterpret_cast<const uint4*>(src + (part * 4 + i) * 1024);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a0 = c ? raw[i].z : raw[i].x, a1 = c ? raw[i].w : raw[i].y;
+              const uint32_t b0 = c ? raw[i].x : raw[i].z, b1 = c ? raw[i].y : raw[i].w;
+              *reinterpret_cast<uint4*>(dst + dst_a + (part * 4 + i) * 1024) =
+                  make_uint4(e4m3x2_to_f16x2(a0 & 0xffffu), e4m3x2_to_f16x2(a0 >> 16), e4m3x2_to_f16x2(a1 & 0xffffu),
+                             e4m3x2_to_f16x2(a1 >> 16));
+              *reinterpret_cast<uint4*>(dst + dst_b + (part * 4 + i) * 1024) =
+                  make_uint4(e4m3x2_to_f16x2(b0 & 0xffffu), e4m3x2_to_f16x2(b0 >> 16), e4m3x2_to_f16x2(b1 & 0xffffu),
+                             e4m3x2_to_f16x2(b1 >> 16));
+            }
+          }
+          fence_proxy_async_smem();  // the generic writes before the tensor core reads the tile
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sm.vr_empty[sr]);
+            mbar_arrive(&sm.v_full[s]);
+          }
         }
       }
     }
   } else {
     reg_alloc<kSoftmaxRegs>();
     // ------------------------------ softmax -------------------------------
+    // A thread's 128 scores leave few registers: what the key loop does not need
+    // is worked out again after it, from the thread index and the piece.
     const int t = warp >> 2;
-    const int r = threadIdx.x & 127;  // row of the tile = TMEM lane
-    const int r_tok = (r * p.g_magic) >> 16;
-    const int tok = tok0 + t * p.tok_tile + r_tok;
-    const bool row_real = r < tile_rows && tok < T;
-    const int nt = t ? n1 : n0;
-    const uint32_t lane_off = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lane_off + t * kBN;
-    const uint32_t tO = tmem + lane_off + 2 * kBN + t * kD;
-    const int visible = !row_real ? 0 : p.causal ? min(S, tok + (S - T) + 1) : S;
-    float sl2 = p.scale_log2;
+    const uint32_t tS = tmem + (uint32_t((warp & 3) * 32) << 16) + t * kBN;
+    constexpr uint32_t kToO = 2 * kBN;  // from S_t to O_t (kD = kBN columns each)
+    static_assert(kD == kBN, "O_t lies as far apart as S_t");
     bool ok = true;
+    int jt = 0;               // key iterations of the CTA, over all pieces
+    int sn = 0, qn = 0;       // key tiles seen, pieces taken part in
+    float sl2 = 0.f;          // score scale of the row, log2 domain
 
-    if (nt > 0) {
-      // q row -> e4m3 hi and lo terms, in place (see the head of this file)
-      ok = __all_sync(0xffffffffu, mbar_wait(&sm.q_full[t], 0, abort_flag));
-      if (ok) {
-        uint32_t w[64];
-        const int sw = r & 7;
+    // q row of the piece -> e4m3 hi and lo terms, in place (see the head of this file)
+    auto make_q = [&](const Piece& pc, int nth) -> bool {
+      if (!__all_sync(0xffffffffu, mbar_wait(&sm.q_full[t], nth & 1, abort_flag))) return false;
+      const int r = thread_index() & 127;  // row of the tile
+      const int r_tok = (r * p.g_magic) >> 16;
+      const bool row_real = r < tile_rows && pc.tok0 + t * p.tok_tile + r_tok < pc.T;
+      uint32_t w[64];
+      const int sw = r & 7;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const uint4 x = *reinterpret_cast<const uint4*>(sm.q[t][c] + r * 128 + ((u ^ sw) << 4));
-            w[c * 32 + u * 4] = x.x, w[c * 32 + u * 4 + 1] = x.y, w[c * 32 + u * 4 + 2] = x.z,
-                           w[c * 32 + u * 4 + 3] = x.w;
-          }
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 64; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
-        const RowScale rs = row_scale(row_real ? max(top & 0xffffu, top >> 16) : 0);
-        sl2 = row_score_scale(sl2, rs);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {  // 16 elements: one 16-byte unit of each term
-          uint4 hi, lo;
-          split_e4m3(*reinterpret_cast<uint32_t(*)[8]>(&w[u * 8]), rs.up, hi, lo);
-          *reinterpret_cast<uint4*>(sm.q[t][0] + r * 128 + ((u ^ sw) << 4)) = hi;
-          *reinterpret_cast<uint4*>(sm.q[t][1] + r * 128 + ((u ^ sw) << 4)) = lo;
+        for (int u = 0; u < 8; ++u) {
+          const uint4 x = *reinterpret_cast<const uint4*>(sm.q[t][c] + r * 128 + ((u ^ sw) << 4));
+          w[c * 32 + u * 4] = x.x, w[c * 32 + u * 4 + 1] = x.y, w[c * 32 + u * 4 + 2] = x.z, w[c * 32 + u * 4 + 3] = x.w;
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_ready[t]);
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 64; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+      const RowScale rs = row_scale(row_real ? max(top & 0xffffu, top >> 16) : 0);
+      sl2 = row_score_scale(p.scale_log2, rs);
+#pragma unroll 1
+      for (int u = 0; u < 8; ++u) {  // 16 elements: one 16-byte unit of each term
+        uint4 hi, lo;
+        split_e4m3(*reinterpret_cast<uint32_t(*)[8]>(&w[0]), rs.up, hi, lo);
+#pragma unroll
+        for (int i = 0; i < 56; ++i) w[i] = w[i + 8];
+        *reinterpret_cast<uint4*>(sm.q[t][0] + r * 128 + ((u ^ sw) << 4)) = hi;
+        *reinterpret_cast<uint4*>(sm.q[t][1] + r * 128 + ((u ^ sw) << 4)) = lo;
       }
-    }
-
-    float m_used = -INFINITY;  // reference max, log2 domain
-    float l = 0.f;             // running row sum relative to m_used
-    auto table_entry = [&](int jj) -> int {
-      const int key0 = (j0 + jj) * kBN;
-      const int nb = min(kBN / 16, (S - key0 + 15) / 16);
-      return lane < nb ? __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + key0 / 16 + lane) : 0;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.q_ready[t]);
+      return true;
     };
-    int entry_next = nt > 0 ? table_entry(0) : 0;
-    for (int j = 0; j < nt && ok; ++j) {
-      const int entry = entry_next;
-      if (j + 1 < nt) entry_next = table_entry(j + 1);
-      ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[t], j & 1, abort_flag));
-      if (!ok) break;
-      tc_fence_after();
-      float s[kBN];
+
+    static_assert((kPieces & (kPieces - 1)) == 0, "slot of piece -1");
+    for (int i = -1; ok; ++i) {  // i = -1 stands before the first piece and makes its q
+      const Piece& pc = sm.piece[i & (kPieces - 1)];
+      if (i >= 0 && !pc.more) break;
+      const int nt = i >= 0 ? pc.n[t] : 0;
+      int left;  // keys of the next tile that the row sees
       {
-        uint32_t u[kBN];
-        tmem_ld128_sync(tS, u);
-#pragma unroll
-        for (int i = 0; i < kBN; ++i) s[i] = __uint_as_float(u[i]);
+        const int r = thread_index() & 127;
+        const int r_tok = (r * p.g_magic) >> 16;
+        const int tok = pc.tok0 + t * p.tok_tile + r_tok;
+        const bool row_real = r < tile_rows && tok < pc.T;
+        left = (!row_real ? 0 : p.causal ? min(pc.S, tok + (pc.S - pc.T) + 1) : pc.S) - pc.j0 * kBN;
       }
-      const int lim = visible - (j0 + j) * kBN;  // visible columns of this tile
-      if (lim < kBN) {
+      float m_used = -INFINITY;  // reference max, log2 domain
+      float l = 0.f;             // running row sum relative to m_used
+      for (int j = 0; j < nt && ok; ++j) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[t], (sn + j) & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        float s[kBN];
+        {
+          uint32_t u[kBN];
+          tmem_ld128_sync(tS, u);
 #pragma unroll
-        for (int i = 0; i < kBN; ++i)
-          if (i >= lim) s[i] = -INFINITY;
-      }
-      {
-        const int nb = min(kBN / 16, (S - (j0 + j) * kBN + 15) / 16);
-        const uint32_t bad = __ballot_sync(
-            0xffffffffu, lane < nb && static_cast<unsigned>(entry) >= static_cast<unsigned>(p.num_blocks));
-        if (bad) {  // warp-uniform
-#pragma unroll
-          for (int g = 0; g < kBN / 16; ++g)
-            if ((bad >> g) & 1u) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) s[g * 16 + i] = -INFINITY;
-            }
+          for (int i = 0; i < kBN; ++i) s[i] = __uint_as_float(u[i]);
         }
+        const uint32_t bad = sm.bad[(jt + j) % kBad];
+        if (left < kBN || bad) {
+#pragma unroll
+          for (int g = 0; g < kBN / 16; ++g) {
+            const int in = ((bad >> g) & 1u) ? 0 : left - g * 16;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (i >= in) s[g * 16 + i] = -INFINITY;
+          }
+        }
+        left -= kBN;
+        float mx8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          mx8[k] = fmaxf(s[k], s[k + 8]);
+#pragma unroll
+          for (int m = 1; m < kBN / 16; ++m) mx8[k] = fmax3(mx8[k], s[k + 16 * m], s[k + 16 * m + 8]);
+        }
+        const float mx = fmaxf(fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), mx8[6]), mx8[7]);
+        const float m_new = fmaxf(m_used, mx * sl2);
+        const bool move = m_new - m_used > kRescaleThreshold;  // false while both are -inf (NaN)
+        if (__any_sync(0xffffffffu, move)) {
+          const bool rescale = move && m_used != -INFINITY;
+          if (__any_sync(0xffffffffu, rescale)) {
+            const float alpha = rescale ? ex2_approx(m_used - m_new) : 1.f;
+            l *= alpha;
+#pragma unroll 1
+            for (int c = 0; c < kD / 32; ++c) {
+              uint32_t u[32];
+              tmem_ld32_sync(tS + kToO + c * 32, u);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
+              tmem_st_x32(tS + kToO + c * 32, u);
+            }
+          }
+          if (move) m_used = m_new;
+        }
+        const float mref = (m_used == -INFINITY) ? 0.f : m_used;
+        const float2 c2 = make_float2(sl2, sl2);
+        const float2 nm2 = make_float2(-mref, -mref);
+        float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                          make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < kBN / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = __ffma2_rn(make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), c2, nm2);
+            const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            sum4[i & 3] = __fadd2_rn(sum4[i & 3], pp);
+            pk[i] = pack_f16x2(pp.x, pp.y);
+          }
+          tmem_st_x16(tS + c * 16, pk);  // P overwrites the first 64 columns of S
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[t]);
+        const float2 s01 = __fadd2_rn(sum4[0], sum4[1]);
+        const float2 s23 = __fadd2_rn(sum4[2], sum4[3]);
+        const float2 sall = __fadd2_rn(s01, s23);
+        l += sall.x + sall.y;
       }
-      float mx8[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        mx8[k] = fmaxf(s[k], s[k + 8]);
-#pragma unroll
-        for (int m = 1; m < kBN / 16; ++m) mx8[k] = fmax3(mx8[k], s[k + 16 * m], s[k + 16 * m + 8]);
+      sn += nt;
+      if (i >= 0) jt += max(pc.n[0], pc.n[1]);
+
+      // The next piece's q, so that its first scores are under way while this
+      // piece's output is stored.
+      if (ok) ok = __all_sync(0xffffffffu, wait_piece(i + 1));
+      const float my_l = l, my_m = m_used;
+      const int had = nt > 0 ? 1 : 0;
+      if (ok) {
+        const Piece& nx = sm.piece[(i + 1) % kPieces];
+        if (nx.more && nx.n[t] > 0) ok = make_q(nx, qn + had);
       }
-      const float mx = fmaxf(fmax3(fmax3(mx8[0], mx8[1], mx8[2]), fmax3(mx8[3], mx8[4], mx8[5]), mx8[6]), mx8[7]);
-      const float m_new = fmaxf(m_used, mx * sl2);
-      const bool move = m_new - m_used > kRescaleThreshold;  // false while both are -inf (NaN)
-      if (__any_sync(0xffffffffu, move)) {
-        const bool rescale = move && m_used != -INFINITY;
-        if (__any_sync(0xffffffffu, rescale)) {
-          const float alpha = rescale ? ex2_approx(m_used - m_new) : 1.f;
-          l *= alpha;
-#pragma unroll
+      if (ok && nt > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[t], qn & 1, abort_flag));
+        tc_fence_after();
+      }
+      if (i < 0) continue;
+      // l = 0: no key seen, o = 0 and lse = -inf; a NaN sum stays NaN.
+      const float inv_l = (my_l == 0.f) ? 0.f : p.v_scale / my_l;
+      const float lse = (my_l == 0.f) ? -INFINITY : (my_m + log2f(my_l)) * 0.69314718055994531f;
+      const bool whole = pc.whole != 0;
+      const int T = pc.T, qoff = pc.qoff, tok_t = pc.tok0 + t * p.tok_tile, head0 = pc.hk * p.G;
+      const int r = thread_index() & 127;
+      const int r_tok = (r * p.g_magic) >> 16, r_head = r - r_tok * p.G, tok = tok_t + r_tok;
+      const bool row_real = r < tile_rows && tok < T;
+      const uint32_t tO = tS + kToO;
+      // Whole rows through the warp's staging area, 64 bytes of each of its 32
+      // rows at a time, 16-byte units XOR-swizzled by row pair so that neither
+      // the row-wise writes nor the reads (four lanes a row) conflict on banks.
+      uint8_t* stage = sm.stage[warp];
+      const int su = (lane >> 1) & 3;
+      if (ok) {
+        if (whole) {
+          const uint64_t o_pol = l2_policy_evict_first();
+#pragma unroll 1
           for (int c = 0; c < kD / 32; ++c) {
             uint32_t u[32];
-            tmem_ld32_sync(tO + c * 32, u);
+            if (nt > 0) {
+              tmem_ld32_sync(tO + c * 32, u);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
-            tmem_st_x32(tO + c * 32, u);
+              for (int e = 0; e < 32; ++e) u[e] = 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                pk[x] = pack_bf16x2(__uint_as_float(u[8 * e + 2 * x]) * inv_l, __uint_as_float(u[8 * e + 2 * x + 1]) * inv_l);
+              *reinterpret_cast<uint4*>(stage + lane * 64 + ((e ^ su) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int rl = e * 8 + (lane >> 2), un = lane & 3;
+              const int rr = (warp & 3) * 32 + rl;
+              const int rt = (rr * p.g_magic) >> 16;
+              const uint4 val = *reinterpret_cast<const uint4*>(stage + rl * 64 + ((un ^ ((rl >> 1) & 3)) << 4));
+              const size_t orow = static_cast<size_t>(qoff) + tok_t + rt;
+              if (rr < tile_rows && tok_t + rt < T && orow < static_cast<size_t>(p.total_q))
+                st_global_v4_hint(reinterpret_cast<uint4*>(p.o + (orow * p.Hq + head0 + rr - rt * p.G) * kD + c * 32) + un,
+                                  val, o_pol);
+            }
+            __syncwarp();
           }
-        }
-        if (move) m_used = m_new;
-      }
-      const float mref = (m_used == -INFINITY) ? 0.f : m_used;
-      const float2 c2 = make_float2(sl2, sl2);
-      const float2 nm2 = make_float2(-mref, -mref);
-      float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                        make_float2(0.f, 0.f)};
+          const size_t orow = static_cast<size_t>(qoff) + tok;
+          if (p.lse != nullptr && row_real && orow < static_cast<size_t>(p.total_q))
+            p.lse[static_cast<size_t>(head0 + r_head) * p.total_q + orow] = lse;
+        } else {
+          float* part = p.part_o + (static_cast<size_t>(pc.slot) * kRows + t * kBM + (warp & 3) * 32) * kD;
+          if (nt > 0) {
+#pragma unroll 1
+            for (int c = 0; c < kD / 16; ++c) {
+              uint32_t u[16];
+              tmem_ld16_sync(tO + c * 16, u);
 #pragma unroll
-      for (int c = 0; c < kBN / 32; ++c) {
-        uint32_t pk[16];
+              for (int e = 0; e < 4; ++e)
+                *reinterpret_cast<float4*>(stage + lane * 64 + ((e ^ su) << 4)) =
+                    make_float4(__uint_as_float(u[4 * e]) * inv_l, __uint_as_float(u[4 * e + 1]) * inv_l,
+                                __uint_as_float(u[4 * e + 2]) * inv_l, __uint_as_float(u[4 * e + 3]) * inv_l);
+              __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 x = __ffma2_rn(make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]), c2, nm2);
-          const float2 pp = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-          sum4[i & 3] = __fadd2_rn(sum4[i & 3], pp);
-          pk[i] = pack_f16x2(pp.x, pp.y);
+              for (int e = 0; e < 4; ++e) {
+                const int rl = e * 8 + (lane >> 2), un = lane & 3;
+                *reinterpret_cast<float4*>(part + rl * kD + c * 16 + un * 4) =
+                    *reinterpret_cast<const float4*>(stage + rl * 64 + ((un ^ ((rl >> 1) & 3)) << 4));
+              }
+              __syncwarp();
+            }
+          }
+          p.part_lse[static_cast<size_t>(pc.slot) * kRows + t * kBM + r] = nt > 0 ? lse : -INFINITY;
         }
-        tmem_st_x16(tS + c * 16, pk);  // P overwrites the first 64 columns of S
       }
-      tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[t]);
-      const float2 s01 = __fadd2_rn(sum4[0], sum4[1]);
-      const float2 s23 = __fadd2_rn(sum4[2], sum4[3]);
-      const float2 sall = __fadd2_rn(s01, s23);
-      l += sall.x + sall.y;
-    }
-
-    if (ok && nt > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_full[t], 0, abort_flag));
-      tc_fence_after();
-    }
-    // Epilogue.  l = 0: no key seen, o = 0 and lse = -inf; a NaN sum stays NaN.
-    const float inv_l = (l == 0.f) ? 0.f : p.v_scale / l;
-    const float lse = (l == 0.f) ? -INFINITY : (m_used + log2f(l)) * 0.69314718055994531f;
-    const bool have_o = ok && nt > 0;  // warp-uniform: tcgen05.ld is warp-wide
-    const size_t row_tok = static_cast<size_t>(qoff) + tok;
-    const int head = hk * p.G + r - r_tok * p.G;
-    const bool store = row_real && row_tok < static_cast<size_t>(p.total_q);
-    if (p.splits > 1) {
-      // fp32 partial, row by row (few rows take this path)
-      const size_t prow = (static_cast<size_t>(split) * p.total_q + row_tok) * p.Hq + head;
-#pragma unroll
-      for (int c = 0; c < kD / 32; ++c) {
-        uint32_t u[32];
-        if (have_o) {
-          tmem_ld32_sync(tO + c * 32, u);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) u[i] = 0u;
-        }
-        if (store) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * kD + c * 32);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(u[4 * i]) * inv_l, __uint_as_float(u[4 * i + 1]) * inv_l,
-                                 __uint_as_float(u[4 * i + 2]) * inv_l, __uint_as_float(u[4 * i + 3]) * inv_l);
-        }
+      if (lane == 0) {
+        if (nt > 0) mbar_arrive(&sm.o_free[t]);
+        mbar_arrive(&sm.piece_free[i % kPieces]);
       }
-      if (store) p.part_lse[prow] = lse;
-    } else {
-      // each warp stages its 32 rows in this tile's q buffer (its MMAs are
-      // done), chunks XOR-swizzled by row, then copies whole rows out
-      uint8_t* stage = sm.q[t][0] + (warp & 3) * 32 * kD * 2;
-      uint8_t* my_row = stage + lane * kD * 2;
-#pragma unroll
-      for (int c = 0; c < kD / 32; ++c) {
-        uint32_t u[32];
-        if (have_o) {
-          tmem_ld32_sync(tO + c * 32, u);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) u[i] = 0u;
-        }
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          pk[i] = pack_bf16x2(__uint_as_float(u[2 * i]) * inv_l, __uint_as_float(u[2 * i + 1]) * inv_l);
-#pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4)
-          *reinterpret_cast<uint4*>(my_row + (((c * 4 + q4) ^ (lane & 15)) << 4)) =
-              make_uint4(pk[4 * q4], pk[4 * q4 + 1], pk[4 * q4 + 2], pk[4 * q4 + 3]);
-      }
-      __syncwarp();
-      const int chunk = lane & 15;
-      const uint64_t o_pol = l2_policy_evict_first();
-#pragma unroll 4
-      for (int pass = 0; pass < 16; ++pass) {
-        const int rl = pass * 2 + (lane >> 4);
-        const int rr = (warp & 3) * 32 + rl;
-        const int rt = (rr * p.g_magic) >> 16;
-        const int otok = tok0 + t * p.tok_tile + rt;
-        const uint4 val = *reinterpret_cast<const uint4*>(stage + rl * kD * 2 + ((chunk ^ (rl & 15)) << 4));
-        const size_t orow = static_cast<size_t>(qoff) + otok;
-        if (rr < tile_rows && otok < T && orow < static_cast<size_t>(p.total_q))
-          st_global_v4_hint(reinterpret_cast<uint4*>(p.o + (orow * p.Hq + hk * p.G + rr - rt * p.G) * kD) + chunk, val,
-                            o_pol);
-      }
-      if (p.lse != nullptr && store) p.lse[static_cast<size_t>(head) * p.total_q + row_tok] = lse;
+      qn += had;
     }
   }
 
@@ -657,54 +954,70 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Merge of the ranges' partials: one warp per (token, query head), rows past
-// the last sequence left alone.  w_i = 2^(lse_i - M); fixed order.
-constexpr int kCombineWarps = 8;
+// Merge of the pieces of cut units: CTA (c, y) takes 64 rows of the unit whose
+// last piece lies on stretch c, a warp eight of them.  Weights 2^(lse_i - M),
+// fixed order.
+constexpr int kMergeRows = 64;
 
-__global__ void __launch_bounds__(kCombineWarps * 32)
-    prefill_fp8_combine(const float* __restrict__ part_o, const float* __restrict__ part_lse,
-                        const int32_t* __restrict__ cu_q, __nv_bfloat16* __restrict__ o, float* __restrict__ lse, int B,
-                        int Hq, int total_q, int splits) {
+__global__ void __launch_bounds__(256) prefill_fp8_merge(const __grid_constant__ Params p) {
   constexpr float kLog2e = 1.4426950408889634f;
-  const int lane = threadIdx.x & 31;
-  const size_t row = static_cast<size_t>(blockIdx.x) * kCombineWarps + (threadIdx.x >> 5);
-  const size_t rows = static_cast<size_t>(total_q) * Hq;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dependency_wait();
   grid_launch_dependents();
-  if (row >= rows || row >= static_cast<size_t>(max(cu_q[B], 0)) * Hq) return;
-  float M = -INFINITY;
-  for (int i = lane; i < splits; i += 32) M = fmaxf(M, part_lse[i * rows + row]);
+  const int c1 = blockIdx.x;
+  const Cut cut = p.cuts[c1];
+  if (cut.c0 < 0) return;
+  const int pieces = c1 - cut.c0 + 1;
+  for (int e = 0; e < kMergeRows / 8; ++e) {
+    const int rr = blockIdx.y * kMergeRows + e * 8 + warp;  // row of the unit
+    const int t = rr / kBM, r = rr % kBM;
+    const int rt = (r * p.g_magic) >> 16;
+    const int tok = cut.tok0 + t * p.tok_tile + rt;
+    const size_t orow = static_cast<size_t>(cut.qoff) + tok;
+    if (r >= p.tok_tile * p.G || tok >= cut.T || orow >= static_cast<size_t>(p.total_q)) continue;
+    auto at = [&](int i) {
+      return (static_cast<size_t>(p.slots) * (cut.c0 + i) + (p.slots > 1 && i + 1 < pieces ? 1 : 0)) * kRows + rr;
+    };
+    float M = -INFINITY, w = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kUnroll = 4;
+    for (int i0 = 0; i0 < pieces; i0 += kUnroll) {
+      float lv[kUnroll];
+      float4 v[kUnroll];
+      bool any = false;
+      float top = M;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  const float Ms = M == -INFINITY ? 0.f : M;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float w = 0.f;
-  constexpr int kUnroll = 4;
-  for (int i0 = 0; i0 < splits; i0 += kUnroll) {
-    float lv[kUnroll];
-    float4 v[kUnroll];
+      for (int u = 0; u < kUnroll; ++u) {
+        const size_t a = at(min(i0 + u, pieces - 1));
+        lv[u] = i0 + u < pieces ? p.part_lse[a] * kLog2e : -INFINITY;
+        v[u] = *reinterpret_cast<const float4*>(p.part_o + a * kD + lane * 4);
+        any |= lv[u] != -INFINITY;  // a NaN counts
+        top = fmaxf(top, lv[u]);
+      }
+      if (!any) continue;
+      const float keep = M == -INFINITY ? 0.f : ex2_approx(M - top);
+      M = top;
+      w *= keep;
+      acc.x *= keep, acc.y *= keep, acc.z *= keep, acc.w *= keep;
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int i = min(i0 + k, splits - 1);
-      lv[k] = i0 + k < splits ? part_lse[i * rows + row] : -INFINITY;
-      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (lv[k] != -INFINITY) v[k] = *reinterpret_cast<const float4*>(part_o + (i * rows + row) * kD + lane * 4);
+      for (int u = 0; u < kUnroll; ++u) {
+        if (lv[u] == -INFINITY) continue;  // an empty piece has no o
+        const float wk = ex2_approx(lv[u] - M);
+        w += wk;
+        acc.x = fmaf(wk, v[u].x, acc.x);
+        acc.y = fmaf(wk, v[u].y, acc.y);
+        acc.z = fmaf(wk, v[u].z, acc.z);
+        acc.w = fmaf(wk, v[u].w, acc.w);
+      }
     }
-#pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const float wk = ex2_approx((lv[k] - Ms) * kLog2e);
-      w += wk;
-      acc.x = fmaf(wk, v[k].x, acc.x);
-      acc.y = fmaf(wk, v[k].y, acc.y);
-      acc.z = fmaf(wk, v[k].z, acc.z);
-      acc.w = fmaf(wk, v[k].w, acc.w);
-    }
+    const float inv = w == 0.f ? 0.f : 1.f / w;
+    const int head = cut.hk * p.G + r - rt * p.G;
+    *reinterpret_cast<uint2*>(p.o + (orow * p.Hq + head) * kD + lane * 4) =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (p.lse != nullptr && lane == 0)
+      p.lse[static_cast<size_t>(head) * p.total_q + orow] =
+          w == 0.f ? -INFINITY : (M + log2f(w)) * 0.69314718055994531f;
   }
-  const float inv = w == 0.f ? 0.f : 1.f / w;
-  *reinterpret_cast<uint2*>(o + row * kD + lane * 4) =
-      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  if (lse != nullptr && lane == 0)
-    lse[(row % Hq) * total_q + row / Hq] = w == 0.f ? -INFINITY : Ms + log2f(w) * 0.69314718055994531f;
 }
 
 }  // namespace prefill8

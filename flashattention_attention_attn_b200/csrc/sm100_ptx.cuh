@@ -282,6 +282,33 @@ __device__ __forceinline__ void umma_ss_f8(uint32_t d_tmem, uint64_t a_desc, uin
       : "memory");
 }
 
+// The same with descriptors as words, for loops whose issuing thread is the
+// bottleneck: the high word is a constant and the low one a base plus a
+// constant (make_sdesc_lo: addresses below 256 KB leave its fields apart).
+template <uint32_t HI>
+__device__ __forceinline__ void umma_ss_f8_words(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc,
+                                                 uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(HI)
+      : "memory");
+}
+template <uint32_t HI>
+__device__ __forceinline__ void umma_ts_words(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc,
+                                              uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(HI)
+      : "memory");
+}
+
 // Arrive on `bar` once every tcgen05 op issued so far by this thread is done.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -315,6 +342,14 @@ __device__ __forceinline__ uint64_t make_sdesc_sw128(uint32_t saddr, uint32_t lb
   d |= 1ull << 46;
   d |= 2ull << 61;
   return d;
+}
+
+// Words of such a descriptor.
+__device__ __forceinline__ uint32_t make_sdesc_lo(uint32_t saddr, uint32_t lbo_bytes) {
+  return (saddr >> 4) | (lbo_bytes >> 4) << 16;
+}
+__host__ __device__ constexpr uint32_t make_sdesc_hi_sw128(uint32_t sbo_bytes) {
+  return (sbo_bytes >> 4) | 1u << 14 | 2u << 29;
 }
 
 // The same with any swizzle: layout 2 = 128-byte, 4 = 64-byte, 6 = 32-byte.
