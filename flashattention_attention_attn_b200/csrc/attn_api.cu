@@ -1152,6 +1152,7 @@ int launch_prefill_fp8(const void* q, const void* kc, const void* vc, const int3
   const long long bound = (static_cast<long long>(total_q) + static_cast<long long>(B) * (rows_cta - 1)) / rows_cta;
   if (bound < units) units = bound;
   units *= Hkv;
+  if (max_tiles > (0x7fffffff / prefill8::kBN) / 2) return ATTN_ERR_UNSUPPORTED;  // unit_keys is an int
   // Short tables have only short units, which are never cut.
   if (num_splits <= 0 && max_tiles <= prefill8::kMinCutTiles) num_splits = 1;
   const int splits_asked = num_splits > 0 ? num_splits : 1;
@@ -1169,7 +1170,7 @@ int launch_prefill_fp8(const void* q, const void* kc, const void* vc, const int3
     p.num_cuts = st->sms;
     if (grid < st->sms) grid = st->sms;
   }
-  if (grid > 0x3fffffffLL || max_tiles > (0x7fffffff / prefill8::kBN) / 2) return ATTN_ERR_UNSUPPORTED;
+  if (grid > 0x3fffffffLL) return ATTN_ERR_UNSUPPORTED;
   void* ws = nullptr;
   if (p.num_cuts > 0) {
     const size_t rows = static_cast<size_t>(p.num_cuts) * p.slots * prefill8::kRows;

@@ -126,6 +126,7 @@ struct __align__(1024) Smem {
   uint32_t v_bad[kVRaw];   // its blocks outside the pool
   uint32_t bad[kBad];      // the same of key iteration i at i % kBad, for the softmax
   long long begin, end, stretch;  // this CTA's stretch of the line
+  long long warp_sum[kThreads / 32][2];  // keys and units of a warp's sequences
   int index;                      // its place among the stretches
   int unit_keys;                  // length of every unit on the line; 0: its keys and kUnitCost
   int b0, mb0;                    // the sequence and query block that it begins in
@@ -275,6 +276,88 @@ __device__ __forceinline__ bool cut_units(long long keys, long long units, int s
   return idle > (waves > 1 ? 32.f : 16.f);
 }
 
+// The line's length, this CTA's stretch of it, and where that begins: a thread
+// sums a run of sequences, the CTA scans the runs, and the thread on whose run
+// the stretch begins looks for the place (one warp walking all sequences took
+// 10 us a CTA with 512 of them).  Kept out of line: inlined, it moved the key
+// loop's code and cost up to 5% of the time (2048 tokens at 32k 912 / 960 us).
+__device__ __noinline__ void find_stretch(const Params& p, Smem& sm) {
+  const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int run0 = min(p.B, static_cast<int>(threadIdx.x) * per), run1 = min(p.B, run0 + per);
+  long long keys = 0, units = 0;
+  for (int b = run0; b < run1; ++b) {
+    const int raw = __ldg(p.seq_lens + b);
+    if (cta == 0 && (raw < 0 || raw > p.max_blocks * 16)) atomicOr(&g_devstatus, kDevStatusBadSeqLen);
+    const Line line(p, 0, b);
+    keys += line.before(line.nb);
+    units += line.nb;
+  }
+  keys *= p.Hkv;
+  units *= p.Hkv;
+  long long keys_end = keys, units_end = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, keys_end, o), y = __shfl_up_sync(0xffffffffu, units_end, o);
+    if (lane >= o) keys_end += x, units_end += y;
+  }
+  if (lane == 31) sm.warp_sum[warp][0] = keys_end, sm.warp_sum[warp][1] = units_end;
+  __syncthreads();
+  long long all_keys = 0, all_units = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const long long x = sm.warp_sum[w][0], y = sm.warp_sum[w][1];
+    if (w < warp) keys_end += x, units_end += y;
+    all_keys += x;
+    all_units += y;
+  }
+  long long stretch = p.stretch;
+  int unit_keys = p.unit_keys;
+  if (stretch == 0) {
+    stretch = unit_keys;
+    if (cut_units(all_keys, all_units, p.sms)) {
+      unit_keys = 0;
+      stretch = (all_keys + p.num_cuts - 1) / p.num_cuts;
+      if (stretch < kMinStretch) stretch = kMinStretch;
+    }
+  }
+  const long long total = unit_keys > 0 ? all_units * unit_keys : all_keys;
+  // The last stretch first: with causal masks the units of a sequence grow.
+  const long long count = min((total + stretch - 1) / stretch, static_cast<long long>(gridDim.x));
+  const int index = cta < count ? static_cast<int>(count) - 1 - cta : cta;
+  const long long begin = stretch * index;
+  const long long end = unit_keys > 0 ? units_end * unit_keys : keys_end;  // of this thread's run
+  long long rest = begin - (end - (unit_keys > 0 ? units * unit_keys : keys));
+  if (rest >= 0 && begin < end) {
+    int b0 = run0, mb0 = 0;
+    for (;; ++b0) {  // ends inside the run: its sequences make up its length
+      const Line line(p, unit_keys, b0);
+      const long long len = line.before(line.nb) * p.Hkv;
+      if (rest < len || b0 + 1 >= run1) break;
+      rest -= len;
+    }
+    const Line line(p, unit_keys, b0);
+    int hi = line.nb;
+    while (hi - mb0 > 1) {  // the last query block that begins at or before `rest`
+      const int mid = (mb0 + hi) / 2;
+      if (line.before(mid) * p.Hkv <= rest)
+        mb0 = mid;
+      else
+        hi = mid;
+    }
+    sm.b0 = b0;
+    sm.mb0 = mb0;
+    sm.rest = rest - line.before(mb0) * p.Hkv;
+  }
+  if (threadIdx.x == 0) {
+    if (begin >= total) sm.b0 = p.B, sm.mb0 = 0, sm.rest = 0;
+    sm.begin = begin;
+    sm.end = min(begin + stretch, total);
+    sm.stretch = stretch;
+    sm.index = index;
+    sm.unit_keys = unit_keys;
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_fp8_sm100(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Params p) {
@@ -323,84 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dependency_wait();
   grid_launch_dependents();
 
-  if (warp == kWarpMma) {
-    // the line's length, this CTA's stretch of it, and where that begins
-    long long keys = 0, units = 0;
-    for (int b = lane; b < p.B; b += 32) {
-      const int raw = __ldg(p.seq_lens + b);
-      if (cta == 0 && (raw < 0 || raw > p.max_blocks * 16)) atomicOr(&g_devstatus, kDevStatusBadSeqLen);
-      const Line line(p, 0, b);
-      keys += line.before(line.nb);
-      units += line.nb;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      keys += __shfl_xor_sync(0xffffffffu, keys, o);
-      units += __shfl_xor_sync(0xffffffffu, units, o);
-    }
-    keys *= p.Hkv;
-    units *= p.Hkv;
-    long long total = units * p.unit_keys, stretch = p.stretch;
-    int unit_keys = p.unit_keys;
-    if (stretch == 0) {
-      stretch = unit_keys;
-      if (cut_units(keys, units, p.sms)) {
-        unit_keys = 0;
-        total = keys;
-        stretch = (total + p.num_cuts - 1) / p.num_cuts;
-        if (stretch < kMinStretch) stretch = kMinStretch;
-      }
-    }
-    // The last stretch first: with causal masks the units of a sequence grow.
-    const long long count = min((total + stretch - 1) / stretch, static_cast<long long>(gridDim.x));
-    const int index = cta < count ? static_cast<int>(count) - 1 - cta : cta;
-    const long long begin = stretch * index;
-    long long before = 0, rest = 0;
-    int b0 = p.B, mb0 = 0;
-    for (int base = 0; base < p.B && b0 == p.B; base += 32) {
-      const int b = base + lane;
-      long long len = 0;
-      if (b < p.B) {
-        const Line line(p, unit_keys, b);
-        len = line.before(line.nb) * p.Hkv;
-      }
-      long long incl = len;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-      }
-      const uint32_t m = __ballot_sync(0xffffffffu, begin < before + incl);
-      if (m != 0) {
-        const int w = __ffs(m) - 1;
-        b0 = base + w;
-        rest = begin - before - __shfl_sync(0xffffffffu, incl - len, w);
-      }
-      before += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (b0 < p.B) {  // the last query block that begins at or before `rest`
-      const Line line(p, unit_keys, b0);
-      int hi = line.nb;
-      while (hi - mb0 > 1) {
-        const int mid = (mb0 + hi) / 2;
-        if (line.before(mid) * p.Hkv <= rest)
-          mb0 = mid;
-        else
-          hi = mid;
-      }
-      rest -= line.before(mb0) * p.Hkv;
-    }
-    if (lane == 0) {
-      sm.begin = begin;
-      sm.end = min(begin + stretch, total);
-      sm.stretch = stretch;
-      sm.index = index;
-      sm.unit_keys = unit_keys;
-      sm.b0 = b0;
-      sm.mb0 = mb0;
-      sm.rest = rest;
-    }
-  }
+  find_stretch(p, sm);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -437,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t kv_pol = l2_policy_evict_last();
       bool ok = true;
       for (int i = 0; ok; ++i) {
-        while (b < p.B && Line(p, unit_keys, b).nb == 0) ++b;
+        while (pos < end && b < p.B && Line(p, unit_keys, b).nb == 0) ++b;
         bool more = pos < end && b < p.B;
         if (more) {
           const long long u = Line(p, unit_keys, b).unit(mb), hi = min(u, lo + (end - pos));

@@ -315,3 +315,94 @@ def test_two_streams_and_a_captured_call():
         for (o, lse), w in zip(outs, want):
             assert torch.equal(o.cpu(), w[0]) and torch.equal(lse.cpu(), w[1])
     assert fa.attn_read_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (6, 1), (16, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_few_long_units_are_cut(causal, Hq, Hkv):
+    """Long keys and few query blocks, where the automatic choice deals the keys
+    out evenly: a unit lies on many stretches, others between them end on one."""
+    ctx, ql = [20000, 0, 9000, 4001, 1, 130], [100, 0, 60, 33, 1, 40]
+    q, cu, c, scale = make(ctx, ql, Hq=Hq, Hkv=Hkv, seed=90 + Hq)
+    o, lse, st = run(q, cu, c, causal, scale, pad=4)
+    assert st == 0
+    check(q, cu, c, causal, scale, o, lse)
+    # the result does not depend on where the blocks lie, nor on what lies behind the ends
+    g = torch.Generator().manual_seed(9)
+    perm = torch.randperm(c.k_cache.shape[0], generator=g)
+    k2, v2, table = torch.empty_like(c.k_cache), torch.empty_like(c.v_cache), c.block_table.clone()
+    k2[perm], v2[perm] = c.k_cache, c.v_cache
+    table[table >= 0] = perm[table[table >= 0].long()].to(torch.int32)
+    for i, L in enumerate(c.seq_lens.tolist()):
+        if L % 16:
+            last = int(table[i, (L - 1) // 16])
+            k2[last, L % 16:] = 0x7F
+            v2[last, L % 16:] = 0xFF
+    e = inputs.PagedInputsFp8(c.q, k2, v2, table, c.seq_lens, 16, c.k_scale, c.v_scale)
+    again = run(q, cu, e, causal, scale, lse=False)
+    assert torch.equal(again[0], o)
+
+
+def test_cut_units_with_ids_outside_the_pool_and_nan_rows():
+    ctx, ql = [9000, 3000, 4000], [70, 40, 50]
+    q, cu, c, scale = make(ctx, ql, Hq=8, Hkv=2, seed=31, spare=20)
+    pool = c.k_cache.shape[0] - 20
+    t = c.block_table.clone()
+    t[0, 3], t[0, 300:330], t[1, 0] = -1, pool + 3, pool
+    t[2, : 4000 // 16] = pool + 7  # nothing left of this sequence
+    e = inputs.PagedInputsFp8(c.q, c.k_cache, c.v_cache, t, c.seq_lens, 16, c.k_scale, c.v_scale)
+    o, lse, st = run(q, cu, e, True, scale, num_blocks=pool)
+    assert st == 0x2
+    check(q, cu, e, True, scale, o, lse, num_blocks=pool)
+    x = q.clone()
+    x[10, 3] = float("nan")
+    o2, lse2, st = run(x, cu, e, True, scale, num_blocks=pool)
+    assert torch.isnan(o2[10, 3]).all() and torch.isnan(lse2[3, 10])
+    o2[10, 3], lse2[3, 10] = o[10, 3], lse[3, 10]
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("B", [385, 800])
+def test_more_sequences_than_threads(B):
+    g = np.random.default_rng(B)
+    ctx = g.integers(0, 150, B).tolist()
+    ql = [int(min(c, x)) for c, x in zip(ctx, g.integers(0, 14, B))]
+    ctx[400 % B], ql[400 % B] = 2500, 90  # tables wide enough for the automatic choice
+    a = make(ctx, ql, Hq=8, Hkv=2, seed=B)
+    for splits in (0, 1, 2):
+        o, lse, st = run(*a[:3], True, a[3], splits=splits, pad=3)
+        assert st == 0
+        check(*a[:3], True, a[3], o, lse)
+
+
+def test_cut_units_on_two_streams_and_captured():
+    import flashattention_attention_attn_b200 as fa
+    jobs, want = [], []
+    for seed, ctx, ql in ((62, [9000, 700], [50, 60]), (63, [6000], [40])):
+        q, cu, c, scale = make(ctx, ql, Hq=8, Hkv=2, seed=seed)
+        o, lse, _ = run(q, cu, c, True, scale)
+        check(q, cu, c, True, scale, o, lse)
+        want.append((o, lse))
+        t = [y.cuda() for y in (q, c.k_cache, c.v_cache, c.block_table, c.seq_lens, cu)]
+        out = (torch.zeros_like(t[0]), torch.zeros(8, q.shape[0], device="cuda"))
+
+        def call(t=t, out=out, c=c, scale=scale, q=q, cu=cu):
+            fa.paged_attn_prefill_fp8(*t, len(cu) - 1, 8, 2, 128, 16, c.block_table.shape[1],
+                                      int((cu[1:] - cu[:-1]).max()), q.shape[0], True, scale, c.k_scale, c.v_scale, 0, *out)
+
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        jobs.append((g, call, out))
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for use_graph in (True, False, True):
+        for _, _, out in jobs:
+            out[0].zero_(), out[1].zero_()
+        torch.cuda.synchronize()
+        for s, (g, call, _) in zip(streams, jobs):
+            with torch.cuda.stream(s):
+                g.replay() if use_graph else call()
+        torch.cuda.synchronize()
+        for (_, _, out), w in zip(jobs, want):
+            assert torch.equal(out[0].cpu(), w[0]) and torch.equal(out[1].cpu(), w[1])
+    assert fa.attn_read_device_status(clear=True) == 0
