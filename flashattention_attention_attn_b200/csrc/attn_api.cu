@@ -1196,7 +1196,7 @@ int prefill_fp8_entry(const void* q, const void* k_cache, const void* v_cache, c
                       cudaStream_t stream) {
   if (max_seqlen_q < 0 || total_q < 0) return ATTN_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale) || !(k_scale > 0.f) || !std::isfinite(k_scale) || !(v_scale > 0.f) ||
-      !std::isfinite(v_scale))
+      !std::isfinite(v_scale) || !std::isfinite(scale * k_scale * 1.4426950408889634f))
     return ATTN_ERR_INVALID_ARG;
   int rc = check_paged_common(B, Hq, Hkv, d, block_size, max_blocks, num_blocks);
   if (rc != ATTN_OK) return rc;

@@ -36,7 +36,9 @@ Plan: block_table [B,max_blocks] is updated in place, the other outputs are
 new; pos_offsets may be None.  Rotary: q [n,Hq,d], k [n,Hkv,d] (rows of heads
 may lie further apart, as columns of a fused projection do), positions
 [axes,n] int32, inv_freq [rot/2] fp32, freq_axis a list of rot/2 axes (empty:
-axis 0); the caches are written in place.
+axis 0); the caches are written in place.  rope_axes' gradient is captured into a
+graph under the rule of every torch operator: no eager graph of the same
+leaves may live on the default stream meanwhile.
 """
 
 from __future__ import annotations
@@ -174,8 +176,10 @@ def _(o_parts, lse_parts):
 
 
 def _rows(x: torch.Tensor) -> torch.Tensor:
-    """x [n, H, d] with the heads of a row side by side, copied only if they are not."""
-    if x.stride(-1) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]) or x.stride(0) % 8 or x.data_ptr() % 16:
+    """x [n, H, d] with the heads of a row side by side and the rows apart, copied only if they are not
+    (a gradient that was expanded over the tokens has rows that share their memory)."""
+    if (x.stride(-1) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]) or x.stride(0) % 8 or x.data_ptr() % 16
+            or (x.shape[0] > 1 and x.stride(0) < x.shape[1] * x.shape[2])):
         return x.contiguous()
     return x
 
@@ -195,6 +199,13 @@ def _need(packed: bool, dtypes, **tensors) -> None:
             raise ValueError(f"{name} must be contiguous")
 
 
+def _shape(**tensors) -> None:
+    """name=(tensor, shape): the sizes that the entry points take from the other tensors; None stands for any."""
+    for name, (x, want) in tensors.items():
+        if x is not None and (x.dim() != len(want) or any(w is not None and n != w for n, w in zip(x.shape, want))):
+            raise ValueError(f"{name} is {tuple(x.shape)}, not {tuple('any' if w is None else w for w in want)}")
+
+
 def _stride(x: torch.Tensor) -> int:
     return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
 
@@ -209,7 +220,9 @@ def paged_cache_plan(block_table: torch.Tensor, cached_lens: torch.Tensor, new_l
                      ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
     _need(True, _INT32, block_table=block_table, cached_lens=cached_lens, new_lens=new_lens, free_blocks=free_blocks,
           pos_offsets=pos_offsets)
+    _shape(block_table=(block_table, (None, None)), free_blocks=(free_blocks, (None,)))
     B, max_blocks = block_table.shape
+    _shape(cached_lens=(cached_lens, (B,)), new_lens=(new_lens, (B,)), pos_offsets=(pos_offsets, (B,)))
     out = [torch.empty(n, device=block_table.device, dtype=torch.int32)
            for n in (B, B + 1, max_tokens, max_tokens, 1)]
     seq_lens, cu, slots, positions, taken = out
@@ -229,7 +242,9 @@ def _rope(call, q, k, positions, inv_freq, freq_axis, adjacent):
     _need(False, _BF16, q=q, k=k)
     _need(False, _INT32, positions=positions)
     _need(True, _FP32, inv_freq=inv_freq)
+    _shape(q=(q, (None, None, None)))
     n, Hq, d = q.shape
+    _shape(k=(k, (n, None, d)), positions=(positions, (None, n)), inv_freq=(inv_freq, (None,)))
     Hkv = k.shape[1]
     q, k, positions = _rows(q), _rows(k), _positions(positions)
     q_out = torch.empty((n, Hq, d), device=q.device, dtype=q.dtype)
@@ -280,15 +295,19 @@ def _append(q, k, v, positions, inv_freq, freq_axis, slot_map, adjacent, k_cache
     _need(True, _INT32, slot_map=slot_map)
     _need(True, _FP32, inv_freq=inv_freq)
     _need(True, _FP8 if scales else _BF16, k_cache=k_cache, v_cache=v_cache)
+    _shape(q=(q, (None, None, None)), k_cache=(k_cache, (None, None, None, None)))
     n, Hq, d = q.shape
-    Hkv = k.shape[1]
+    num_blocks, block_size, Hkv = k_cache.shape[:3]
+    _shape(k=(k, (n, Hkv, d)), v=(v, (n, Hkv, d)), positions=(positions, (None, n)), inv_freq=(inv_freq, (None,)),
+           slot_map=(slot_map, (n,)), k_cache=(k_cache, (num_blocks, block_size, Hkv, d)),
+           v_cache=(v_cache, (num_blocks, block_size, Hkv, d)))
     q, k, v, positions = _rows(q), _rows(k), _rows(v), _positions(positions)
     q_out = torch.empty((n, Hq, d), device=q.device, dtype=q.dtype)
     call = _binding.rope_axes_paged_append_fp8 if scales else _binding.rope_axes_paged_append
     with torch.cuda.device(q.device):
         call(q, k, v, positions, inv_freq, freq_axis or None, slot_map, n, Hq, Hkv, d, 2 * inv_freq.numel(),
-             positions.shape[0], positions.stride(0), _stride(q), _stride(k), _stride(v), adjacent, k_cache.shape[1],
-             k_cache.shape[0], *scales, q_out, k_cache, v_cache)
+             positions.shape[0], positions.stride(0), _stride(q), _stride(k), _stride(v), adjacent, block_size,
+             num_blocks, *scales, q_out, k_cache, v_cache)
     return q_out
 
 
@@ -325,10 +344,14 @@ def paged_attn_prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     _need(False, _BF16, q=q)
     _need(True, _FP8, k_cache=k_cache, v_cache=v_cache)
     _need(True, _INT32, block_table=block_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q)
+    _shape(q=(q, (None, None, None)), k_cache=(k_cache, (None, None, None, None)),
+           cu_seqlens_q=(cu_seqlens_q, (None,)))
     q = q.contiguous()
     total_q, Hq, d = q.shape
-    num_blocks, block_size, Hkv = k_cache.shape[0], k_cache.shape[1], k_cache.shape[2]
+    num_blocks, block_size, Hkv = k_cache.shape[:3]
     B = cu_seqlens_q.shape[0] - 1
+    _shape(k_cache=(k_cache, (num_blocks, block_size, Hkv, d)), v_cache=(v_cache, (num_blocks, block_size, Hkv, d)),
+           block_table=(block_table, (B, None)), seq_lens=(seq_lens, (B,)))
     o = torch.empty((total_q, Hq, d), device=q.device, dtype=q.dtype)
     lse = torch.empty((Hq, total_q), device=q.device, dtype=torch.float32)
     if B > 0:

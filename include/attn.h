@@ -558,9 +558,10 @@ int rope_axes_paged_append_fp8(const void* q, const void* k, const void* v, cons
  * chunks of any size down to one token per sequence.
  *
  *   k_cache, v_cache [num_blocks, 16, Hkv, 128] e4m3 bytes; num_splits: the
- *   key range of each sequence is cut into at most num_splits ranges of whole
- *   128-key tiles whose partial results are merged; <= 0 picks a value that
- *   fills the GPU.  All other arguments and the result as paged_attn_prefill.
+ *   table row's max_blocks are cut into at most num_splits ranges of whole
+ *   128-key tiles whose partial results are merged; <= 0: the kernel divides
+ *   the work by the sequences' lengths, which it reads on the device.  All
+ *   other arguments and the result as paged_attn_prefill.
  *   Output rows behind the last sequence (total_q > cu_seqlens_q[B]) are left
  *   as they were.  Deterministic; the result does not depend on the blocks'
  *   physical placement.
@@ -570,12 +571,17 @@ int rope_axes_paged_append_fp8(const void* q, const void* k, const void* v, cons
  *   2^-9 of the row's largest (2^-18 of the largest below); the weights are
  *   rounded to f16 before they meet V; sums are fp32.  Cached values that a
  *   sequence holds are assumed finite; slots past its end may hold anything.
- *   Workspace: with more than one range, ranges * total_q * Hq * 129 fp32 from
- *   the library's stream-ordered pool.
+ *   Workspace, from the library's stream-ordered pool (a graph memory node
+ *   in a stream capture): with num_splits <= 0 at most 40 MB, the partial
+ *   results of two pieces an SM; otherwise, with more than one range, at most
+ *   256 * 129 fp32 for every range of every 256 query rows of a kv head (a
+ *   sequence's last rows count as 256).
  *   Supported: d == 128; block_size == 16; Hq / Hkv <= 128; max_blocks < 2^27;
  *   16-byte aligned q, caches and o; sm_100.  Errors: as paged_attn_prefill;
  *   ATTN_ERR_INVALID_ARG also for a k_scale or v_scale that is not finite and
- *   positive.
+ *   positive, or a product of scale and k_scale that is not finite;
+ *   ATTN_ERR_UNSUPPORTED also where B * (max_blocks / 8 + 3) tiles or the
+ *   CTAs (num_splits > 0: ranges times query blocks) pass 2^30.
  */
 int paged_attn_prefill_fp8(const void* q, const void* k_cache, const void* v_cache,
                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_seqlens_q,

@@ -194,6 +194,46 @@ def test_rope_op_trains():
 
 
 @pytest.mark.gpu
+def test_rope_op_takes_an_expanded_gradient_and_a_captured_step():
+    """A gradient whose rows share their memory; forward and backward captured
+    while an eager graph of the same leaves lives, made on the stream of the
+    capture (made on the default stream it stops the capture of any torch
+    operator's backward, x * 2 as well)."""
+    import flashattention_attention_attn_b200.torch_ops  # noqa: F401
+    n, H, d = 29, 3, 64
+    g = torch.Generator().manual_seed(6)
+    q, k = (torch.randn(n, H, d, generator=g).to(BF16).cuda().requires_grad_() for _ in range(2))
+    pos = torch.randint(0, 3000, (1, n), generator=g, dtype=torch.int32).cuda()
+    f = torch.rand(d // 2, generator=g).cuda()
+    row = torch.randn(H, d, generator=g).to(BF16).cuda()
+    want = ps.rope_axes(f64(row.expand(n, H, d)), pos.cpu().numpy(), f64(f), [0] * (d // 2), False, sign=-1.0)
+
+    def grads():
+        a, b = torch.ops.fa_b200.rope_axes(q, k, pos, f, [], False)
+        return torch.autograd.grad((a, b), (q, k), (row.expand(n, H, d), row.expand(n, H, d)))
+
+    for got in grads():
+        assert np.all(np.abs(f64(got) - want) <= 2.0 ** -8 * np.abs(want) + 1e-5)
+    q, k = (x.detach().requires_grad_() for x in (q, k))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        alive = sum(x.sum() for x in torch.ops.fa_b200.rope_axes(q, k, pos, f, [], False))
+        grads()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        captured = grads()
+    with torch.no_grad():
+        row.mul_(2)
+    graph.replay()
+    torch.cuda.synchronize()
+    for got in captured:
+        assert np.all(np.abs(f64(got) - 2 * want) <= 2.0 ** -7 * np.abs(want) + 2e-5)
+    assert all(torch.isfinite(x).all() for x in torch.autograd.grad(alive, (q, k)))
+
+
+@pytest.mark.gpu
 def test_tensors_off_the_current_device_are_refused():
     import flashattention_attention_attn_b200 as fa
     x = torch.zeros(4, 128, dtype=BF16, device="cuda")

@@ -227,3 +227,43 @@ def test_oracle_e4m3_against_torch():
                        [v, -v, (v[1:] + v[:-1]) / 2])
     t = torch.from_numpy(x).float().clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
     assert np.array_equal(ps.nearest_e4m3(x.astype(np.float32)), t)
+
+
+@pytest.mark.parametrize("scale,ks", [(1e30, 1e30), (3e38, 1.0)])
+def test_prefill_fp8_refuses_a_product_of_scales_past_fp32(lib, scale, ks):
+    assert _chunk(lib, scale=scale, ks=ks) == INVALID
+
+
+def test_ops_refuse_sizes_that_do_not_fit():
+    """What a call would read past: refused before anything is launched."""
+    import flashattention_attention_attn_b200.torch_ops  # noqa: F401
+    ops = torch.ops.fa_b200
+    i32, bf = dict(dtype=torch.int32), dict(dtype=torch.bfloat16)
+    B, n = 3, 10
+    table, lens, free, f = torch.zeros(B, 4, **i32), torch.zeros(B, **i32), torch.zeros(9, **i32), torch.ones(64)
+    q, k, pos, slots = torch.zeros(n, 4, 128, **bf), torch.zeros(n, 2, 128, **bf), torch.zeros(2, n, **i32), torch.zeros(n, **i32)
+    kc, k8 = torch.zeros(9, 16, 2, 128, **bf), torch.zeros(9, 16, 2, 128, dtype=torch.uint8)
+    cu = torch.zeros(B + 1, **i32)
+
+    def refused(name, op, *args):
+        with pytest.raises(ValueError, match=name):
+            op(*args)
+
+    refused("new_lens", ops.paged_cache_plan, table, lens, lens[:2], free, None, n)
+    refused("cached_lens", ops.paged_cache_plan, table, cu, lens, free, None, n)
+    refused("pos_offsets", ops.paged_cache_plan, table, lens, lens, free, cu, n)
+    refused("block_table", ops.paged_cache_plan, lens, lens, lens, free, None, n)
+    refused("k is", ops.rope_axes, q, k[:9], pos, f, [], False)
+    refused("k is", ops.rope_axes, q, torch.zeros(n, 2, 64, **bf), pos, f, [], False)
+    refused("positions", ops.rope_axes, q, k, pos[:, :9], f, [], False)
+    refused("positions", ops.rope_axes, q, k, pos[0], f, [], False)
+    for op, c, scales in ((ops.rope_axes_paged_append, kc, ()), (ops.rope_axes_paged_append_fp8, k8, (1.0, 1.0))):
+        refused("slot_map", op, q, k, k, pos, f, [], slots[:9], False, c, c.clone(), *scales)
+        refused("v is", op, q, k, q, pos, f, [], slots, False, c, c.clone(), *scales)
+        refused("k is", op, q, q, k, pos, f, [], slots, False, c, c.clone(), *scales)
+        refused("v_cache", op, q, k, k, pos, f, [], slots, False, c, c[:8].clone(), *scales)
+    args = (True, 0.1, 1.0, 1.0, 0)
+    refused("v_cache", ops.paged_attn_prefill_fp8, q, k8, k8[:5], table, lens, cu, 8, *args)
+    refused("k_cache", ops.paged_attn_prefill_fp8, q[..., :64], k8, k8, table, lens, cu, 8, *args)
+    refused("block_table", ops.paged_attn_prefill_fp8, q, k8, k8, table[:2], lens, cu, 8, *args)
+    refused("seq_lens", ops.paged_attn_prefill_fp8, q, k8, k8, table, cu, cu, 8, *args)
