@@ -32,14 +32,16 @@
 //
 // Work split.  A unit is (two query tiles of a sequence, kv head).  The units lie
 // one behind the other on a line and every CTA takes a stretch of it.  Either a
-// stretch is a unit, the longest of a sequence first, and CTAs are handed out as
-// SMs fall free; or one CTA to an SM takes an equal share of all keys, whatever
-// the lengths are, and works through the pieces of units on it (cut_units has the
-// choice, made from the lengths on the device).  There the copies run ahead into
-// the next piece, its q is made ready before the output of the piece before is
-// stored, and its first scores are under way meanwhile.  The pieces of a unit
-// that a stretch's end cuts go to the workspace in fp32 (at most two a stretch)
-// and prefill_fp8_merge joins them.
+// stretch is a unit, the longest of a sequence first, and a CTA near the end of
+// one calls off the start of the grid's next CTA and takes its unit too; or one
+// CTA to an SM takes an equal share of all keys, whatever the lengths are, and
+// works through the pieces of units on it (cut_units has the choice, made from
+// the lengths on the device).  Either way the copies run ahead into the next
+// piece, its q is made ready before the output of the piece before is stored, and
+// its first scores are under way meanwhile (a CTA for each unit instead: 8 x 512
+// tokens 239 us instead of 217).  The pieces of a unit that a stretch's end cuts
+// go to the workspace in fp32 (at most two a stretch) and prefill_fp8_merge
+// joins them.
 //
 // What bounds it: a key iteration (two query tiles x 128 keys) is one chain a
 // query tile, softmax 0.9 us, PV and the next QK 0.55 us, and hand-overs, at
@@ -49,8 +51,8 @@
 // Straight-line code is kept short (loops over chunks of the output, of q and of
 // V stay rolled): what runs once a piece is fetched cold.
 // Measured, G = 4, 8 kv heads: 2048 tokens at 32k 906 us (1.2 PFLOP/s of 16-bit
-// work), 8 x 512 tokens at .5k to 7.7k 236 us, 4096 tokens from nothing 163 us;
-// 33 sequences of 0 to 300 tokens at 0 to 2500, G = 6, 4 kv heads, 196 us.
+// work), 8 x 512 tokens at .5k to 7.7k 217 us, 4096 tokens from nothing 150 us;
+// 33 sequences of 0 to 300 tokens at 0 to 2500, G = 6, 4 kv heads, 184 us.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -121,12 +123,16 @@ struct __align__(1024) Smem {
   uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
   uint64_t piece_full[kPieces], piece_free[kPieces];
   uint64_t mma_done;
+  uint64_t next_full;      // the answer to a request for another unit
+  alignas(16) uint32_t next[4];
   Piece piece[kPieces];
   int v_valid[kVRaw];      // keys of the raw tile inside the sequence
   uint32_t v_bad[kVRaw];   // its blocks outside the pool
   uint32_t bad[kBad];      // the same of key iteration i at i % kBad, for the softmax
   long long begin, end, stretch;  // this CTA's stretch of the line
   long long warp_sum[kThreads / 32][2];  // keys and units of a warp's sequences
+  int run_end[kThreads];          // units up to the end of each thread's run of sequences
+  int count;                      // stretches
   int index;                      // its place among the stretches
   int unit_keys;                  // length of every unit on the line; 0: its keys and kUnitCost
   int b0, mb0;                    // the sequence and query block that it begins in
@@ -136,6 +142,7 @@ struct __align__(1024) Smem {
 };
 
 constexpr size_t smem_bytes() { return sizeof(Smem); }
+static_assert(sizeof(Smem) <= 232448, "shared memory of a CTA");
 
 // A cut unit, written for the stretch that holds its last piece.
 struct Cut {
@@ -160,7 +167,7 @@ struct Params {
   int total_q, causal;
   int slots;                   // workspace slots of a stretch: 2, or 1 when it is one piece
   // keys of a stretch, with every unit unit_keys long; 0: the kernel decides
-  // between a unit a CTA (unit_keys each) and num_cuts equal stretches
+  // between whole units (unit_keys each) and num_cuts equal stretches
   long long stretch;
   int unit_keys;
   int sms;
@@ -259,15 +266,16 @@ struct Line {
   }
 };
 
-// Whether the line is cut into even stretches, or every CTA takes a unit.
-// A unit a CTA, handed out as CTAs end, leaves SMs idle while the last ones run:
-// for units of one length L it is L (ceil(u) - u) key tiles with u units an SM;
-// other lengths fill in, the more the larger u is.  Cutting costs the pieces'
-// workspace, their merge, and one more start and end an SM, which together took
-// as long as 15 to 30 key tiles.  Measured with 8 kv heads, G = 4, a unit a CTA /
-// cut: 2048 tokens at 32k (u = 1.7, L = 248) 1000 / 906 us; 2 x 2048 at 8k to 24k
-// (1.7, 125) 937 / 865; 6 x 512 at 1k to 8k (2.6, 35) 259 / 253; 4 x 512 at 1k to
-// 8k (1.7, 35) 149 / 174; 8 x 512 at .5k to 7.7k (3.3, 24) 239 / 276.
+// Whether the line is cut into even stretches, or a CTA takes units as they come.
+// Whole units leave SMs idle while the last ones run: for units of one length L
+// it is L (ceil(u) - u) key tiles with u units an SM; other lengths fill in, the
+// more the larger u is.  Cutting costs the pieces' workspace, their merge, and
+// one more start and end an SM, which together took as long as 15 to 30 key
+// tiles.  Measured with 8 kv heads, G = 4, whole units / cut: 2048 tokens at 32k
+// (u = 1.7, L = 248) 1000 / 925 us; 1536 at 8k (1.3, 69) 284 / 237; 256 at 30k
+// (.2, 234) 475 / 148; 2 x 2048 at 8k to 24k (1.7, 125) 900 / 895; 6 x 512 at 1k to
+// 8k (2.6, 35) 223 / 265; 4 x 512 at 1k to 8k (1.7, 35) 145 / 187; 8 x 512 at .5k to
+// 7.7k (3.3, 24) 217 / 325.
 __device__ __forceinline__ bool cut_units(long long keys, long long units, int sms) {
   if (units == 0) return false;
   const float len = static_cast<float>(keys) / static_cast<float>(units) - kUnitCost;
@@ -279,7 +287,7 @@ __device__ __forceinline__ bool cut_units(long long keys, long long units, int s
 // The line's length, this CTA's stretch of it, and where that begins: a thread
 // sums a run of sequences, the CTA scans the runs, and the thread on whose run
 // the stretch begins looks for the place (one warp walking all sequences took
-// 10 us a CTA with 512 of them).  Kept out of line: inlined, it moved the key
+// 10 us with 512 of them).  Kept out of line: inlined, it moved the key
 // loop's code and cost up to 5% of the time (2048 tokens at 32k 912 / 960 us).
 __device__ __noinline__ void find_stretch(const Params& p, Smem& sm) {
   const int cta = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -324,6 +332,7 @@ __device__ __noinline__ void find_stretch(const Params& p, Smem& sm) {
   // The last stretch first: with causal masks the units of a sequence grow.
   const long long count = min((total + stretch - 1) / stretch, static_cast<long long>(gridDim.x));
   const int index = cta < count ? static_cast<int>(count) - 1 - cta : cta;
+  sm.run_end[threadIdx.x] = static_cast<int>(min(units_end, 0x7fffffffLL));
   const long long begin = stretch * index;
   const long long end = unit_keys > 0 ? units_end * unit_keys : keys_end;  // of this thread's run
   long long rest = begin - (end - (unit_keys > 0 ? units * unit_keys : keys));
@@ -353,9 +362,37 @@ __device__ __noinline__ void find_stretch(const Params& p, Smem& sm) {
     sm.begin = begin;
     sm.end = min(begin + stretch, total);
     sm.stretch = stretch;
+    sm.count = static_cast<int>(count);
     sm.index = index;
     sm.unit_keys = unit_keys;
   }
+}
+
+// Cluster launch control: calls off the start of the next CTA of the grid; the
+// answer (whether there was one, and which) arrives on next_full.
+__device__ __forceinline__ void ask_for_unit(Smem& sm) {
+  fence_proxy_async_smem();  // the answer before has been read
+  mbar_arrive_expect_tx(&sm.next_full, 16);
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(sm.next)),
+               "r"(smem_u32(&sm.next_full))
+               : "memory");
+}
+
+// The CTA that was called off, -1: none was left (after which no more may be asked).
+__device__ __forceinline__ int answered_cta(const Smem& sm) {
+  int cta;
+  asm volatile(
+      "{\n\t.reg .b128 a;\n\t.reg .b64 lo, hi;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.v2.b64 {lo, hi}, [%1];\n\t"
+      "mov.b128 a, {lo, hi};\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, a;\n\t}"
+      : "=r"(cta)
+      : "r"(smem_u32(sm.next))
+      : "memory");
+  return cta;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -393,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.piece_free[i], 8 + 1 + kConvWarps);
     }
     mbar_init(&sm.mma_done, 1);
+    mbar_init(&sm.next_full, 1);
     sm.abort_flag = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&tmQ);
@@ -424,11 +462,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Walks the stretch for the whole CTA.  Lane L < 8 issues K's copy of
       // block L of the tile, lane 8 + L V's.
       long long pos = sm.begin, lo = 0;
-      const long long end = sm.end;
+      long long end = sm.end;
       int b = sm.b0, mb = sm.mb0, hk = 0;
       // The unit's first places hold no key: an end of a stretch among them
       // counts as the unit's beginning, so that no piece is without a key.
       const int unit_keys = sm.unit_keys, index = sm.index;
+      const bool takes_units = unit_keys > 0 && sm.stretch == unit_keys;
+      int asked = 0;  // requests for another unit
       const int cost = unit_keys > 0 ? 0 : kUnitCost;
       if (b < p.B) {
         const long long u = Line(p, unit_keys, b).unit(mb);
@@ -443,6 +483,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t kv_pol = l2_policy_evict_last();
       bool ok = true;
       for (int i = 0; ok; ++i) {
+        if (i > 0 && takes_units) {
+          // The next unit is that of a CTA not yet started, whose start is called off.
+          int other = -1;
+          if (lane == 0) {
+            if (asked < i) ask_for_unit(sm), ++asked;
+            ok = mbar_wait(&sm.next_full, (i - 1) & 1, abort_flag);
+            if (ok) other = answered_cta(sm);
+          }
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          other = __shfl_sync(0xffffffffu, other, 0);
+          asked = i;
+          if (!ok) break;
+          const int unit = other < 0 || other >= sm.count ? -1 : sm.count - 1 - other;
+          const int slot = unit < 0 ? other : unit;
+          if (lane == 0 && slot >= 0 && slot < p.num_cuts) p.cuts[slot].c0 = -1;
+          b = p.B;
+          if (unit >= 0) {
+            const uint32_t w = __ballot_sync(0xffffffffu, lane < kThreads / 32 && sm.run_end[min(lane, kThreads / 32 - 1) * 32 + 31] > unit);
+            const int w0 = __ffs(w) - 1;
+            const int r = w0 * 32 + __ffs(__ballot_sync(0xffffffffu, sm.run_end[w0 * 32 + lane] > unit)) - 1;
+            const int per = (p.B + kThreads - 1) / kThreads;
+            int rest = unit - (r > 0 ? sm.run_end[r - 1] : 0);
+            for (b = r * per;; ++b) {
+              const int n = Line(p, unit_keys, b).nb * p.Hkv;
+              if (rest < n) break;
+              rest -= n;
+            }
+            mb = rest / p.Hkv;
+            hk = rest - mb * p.Hkv;
+            pos = lo = 0;
+            end = unit_keys;
+          }
+        }
         while (pos < end && b < p.B && Line(p, unit_keys, b).nb == 0) ++b;
         bool more = pos < end && b < p.B;
         if (more) {
@@ -496,6 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok || !more) break;
         if (n_max == 0) continue;
+        const int ask_at = max(n_max - 2, 0);  // not earlier: a unit is taken by who is about to be free
         if (lane == 0) {
           const int lead = (pc.n[1] >= pc.n[0] && pc.n[1] > 0) ? 1 : 0;
           for (int e = 0; e < 2 && ok; ++e) {
@@ -520,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int valid = min(kBN, pc.S - blk0 * 16);
           const int nblk = (valid + 15) / 16;
           const int id = id_next;
+          if (takes_units && j == ask_at && lane == 0) ask_for_unit(sm), asked = i + 1;
           if (j + 1 < n_max) id_next = blk0 + 8 + il < nblk_all ? __ldg(table + blk0 + 8 + il) : 0;
           const uint32_t bad = __ballot_sync(
               0xffffffffu, lane < nblk && static_cast<unsigned>(id) >= static_cast<unsigned>(p.num_blocks));
@@ -557,6 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // let the copies already issued land before shared memory is released
         if (part0 > 0) mbar_wait_drain(&sm.q_full[0], (part0 - 1) & 1);
         if (part1 > 0) mbar_wait_drain(&sm.q_full[1], (part1 - 1) & 1);
+        if (asked > 0) mbar_wait_drain(&sm.next_full, (asked - 1) & 1);
         for (int j = max(0, jt - kKStages); j < jt; ++j) mbar_wait_drain(&sm.k_full[j % kKStages], (j / kKStages) & 1);
         for (int j = max(0, jt - kVRaw); j < jt; ++j) mbar_wait_drain(&sm.vr_full[j % kVRaw], (j / kVRaw) & 1);
       }
