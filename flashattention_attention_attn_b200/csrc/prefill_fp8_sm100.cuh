@@ -1036,10 +1036,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Merge of the pieces of cut units: CTA (c, y) takes 64 rows of the unit whose
-// last piece lies on stretch c, a warp eight of them.  Weights 2^(lse_i - M),
+// Merge of the pieces of cut units: CTA (c, y) takes 32 rows of the unit whose
+// last piece lies on stretch c, a warp four of them.  Weights 2^(lse_i - M),
 // fixed order.
-constexpr int kMergeRows = 64;
+constexpr int kMergeRows = 32;
 
 __global__ void __launch_bounds__(256) prefill_fp8_merge(const __grid_constant__ Params p) {
   constexpr float kLog2e = 1.4426950408889634f;
