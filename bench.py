@@ -65,11 +65,11 @@ DEFAULT_WORKLOAD = "long"
 # bench reports null until a new capture replaces it.
 TRAFFIC = {
     # set: {"prefill": bytes per launch, "decode": bytes per call (split + combine), "csrc": hash}
-    "long": {"prefill": 381.92e6, "decode": 539.75e6, "csrc": "c2db8360f1659fcb"},
-    "step": {"prefill": 12.65e6, "decode": 604.99e6, "csrc": "c2db8360f1659fcb"},
-    "fp8": {"prefill": 12.65e6, "decode": 306.29e6, "csrc": "c2db8360f1659fcb"},
-    "varlen": {"prefill": 279.62e6, "decode": 605.21e6, "csrc": "c2db8360f1659fcb"},
-    "chunked": {"prefill": 209.72e6, "decode": 605.10e6, "csrc": "c2db8360f1659fcb"},
+    "long": {"prefill": 385.87e6, "decode": 539.64e6, "csrc": "9898647b944a1719"},
+    "step": {"prefill": 12.65e6, "decode": 605.03e6, "csrc": "9898647b944a1719"},
+    "fp8": {"prefill": 12.65e6, "decode": 306.21e6, "csrc": "9898647b944a1719"},
+    "varlen": {"prefill": 279.74e6, "decode": 605.02e6, "csrc": "9898647b944a1719"},
+    "chunked": {"prefill": 209.86e6, "decode": 605.07e6, "csrc": "9898647b944a1719"},
 }
 
 
