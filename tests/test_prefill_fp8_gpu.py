@@ -406,3 +406,42 @@ def test_cut_units_on_two_streams_and_captured():
         for (_, _, out), w in zip(jobs, want):
             assert torch.equal(out[0].cpu(), w[0]) and torch.equal(out[1].cpu(), w[1])
     assert fa.attn_read_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("splits", [0, 1, 2])
+def test_more_units_than_sms_on_two_streams_and_captured(splits):
+    """Hundreds of units, which running CTAs take over from the grid, in two
+    calls at once, eager and replayed: the same bits as one call alone."""
+    import flashattention_attention_attn_b200 as fa
+    jobs = []
+    for seed, B in ((64, 41), (65, 23)):
+        g = np.random.default_rng(seed)
+        ctx = g.integers(0, 2200, B).tolist()
+        ql = [int(min(c, x)) for c, x in zip(ctx, g.integers(0, 200, B))]
+        ctx[3], ql[3] = 2300, 200
+        q, cu, c, scale = make(ctx, ql, seed=seed)
+        want = run(q, cu, c, True, scale, splits=splits)
+        check(q, cu, c, True, scale, *want[:2])
+        t = [y.cuda() for y in (q, c.k_cache, c.v_cache, c.block_table, c.seq_lens, cu)]
+        out = (torch.zeros_like(t[0]), torch.zeros(32, q.shape[0], device="cuda"))
+
+        def call(t=t, out=out, c=c, scale=scale, q=q, cu=cu, B=B):
+            fa.paged_attn_prefill_fp8(*t, B, 32, 8, 128, 16, c.block_table.shape[1], int((cu[1:] - cu[:-1]).max()),
+                                      q.shape[0], True, scale, c.k_scale, c.v_scale, splits, *out)
+
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        jobs.append((graph, call, out, want))
+    streams = [torch.cuda.Stream() for _ in jobs]
+    for use_graph in (True, False, True, False):
+        for _, _, out, _ in jobs:
+            out[0].zero_(), out[1].zero_()
+        torch.cuda.synchronize()
+        for s, (graph, call, _, _) in zip(streams, jobs):
+            with torch.cuda.stream(s):
+                graph.replay() if use_graph else call()
+        torch.cuda.synchronize()
+        for _, _, out, want in jobs:
+            assert torch.equal(out[0].cpu(), want[0]) and torch.equal(out[1].cpu(), want[1])
+    assert fa.attn_read_device_status(clear=True) == 0
