@@ -8,20 +8,24 @@
 // longer than the tile's bytes.  Here the products are turned round, keys and
 // head dim on the 128 lanes and the rows on the columns:
 //   S^T [128 keys x 2R] = K [keys x d] (Q_hi ; Q_lo)^T
-//   O^T [128 d x 4R]   += V^T [d x keys] (P_0 ; P_1 ; P_2 ; P_3)
+//   O^T [128 d x 3R]   += V^T [d x keys] (P_0 ; P_1 ; P_2)
 // K and V go to the 8-bit MMAs as the e4m3 codes they are (V read transposed),
 // nothing is converted, and a thread owns one key: R exponentials a tile.
 //
 // q is split into two e4m3 terms as in the other kernel; both stand side by
 // side in the N dimension of one MMA and a thread adds its two columns.  The
-// weights are rounded to f16 and split exactly into four e5m2 terms (an e5m2
-// number is the top byte of an f16: each term takes three of the eleven bits
-// left, the rest is the exact f16 difference); the four products are added at
-// the end.  Two e4m3 terms would need half the columns, but their smallest step
-// of 2^-9 leaves few bits to weights far below the row's largest one, and a
-// long row can hold most of its sum in those.  e5m2 reaches 2^-16: with
-// p = 2^(x - m + 7) and m within 8 of the running maximum, p lies in (0, 2^15]
-// and weights keep their bits down to 2^-20 of the largest.
+// weights are rounded to f16 and split into three signed e5m2 terms, p = t_0 +
+// t_1 / 2^4 + t_2 / 2^8.  An e5m2 number is the top byte of an f16, three
+// significant bits: t_0 is p rounded to that, the rest (an exact f16 difference,
+// at most 2^-3 of p) is taken times 16, and so on.  With p = 2^(x - m + 6)
+// and m within 8 of the running maximum, p lies in (0, 2^14], no term overflows,
+// and the split is exact for every f16 in that range, subnormal ones included:
+// without the factors of 16 the terms would end at 2^-16, e5m2's smallest step,
+// and weights far below the row's largest, which can make up most of a long
+// row's sum, would lose their bits.  So weights have their 11 bits down to 2^-20
+// of the row's largest and an error of at most 2^-31 of it below.  The three
+// products are weighted and added at the end.  Two e4m3 terms would need fewer
+// columns, but their smallest step is 2^-9.
 //
 // The reference m of a row moves only when a score exceeds it by more than 8:
 // the four softmax warps note it and arrive on a barrier, make their
@@ -62,8 +66,8 @@ constexpr int kFewMinChunk = 4;    // length of a stretch at least
 // Length that a sequence adds to its tiles on the line: a piece's q, its first tile
 // (which sets the references) and its end take about as long as three tiles.
 constexpr int kFewPieceCost = 3;
-constexpr float kFewShift = 7.0f;  // p = 2^(x - m + 7)
-constexpr float kFewLimit = 15.0f;  // exponents above this move m
+constexpr float kFewShift = 6.0f;  // p = 2^(x - m + 6)
+constexpr float kFewLimit = 14.0f;  // exponents above this move m
 constexpr float kFewUnseen = 1e30f;  // offset of a row that has seen no key
 
 template <int R>
@@ -72,13 +76,15 @@ struct FewConfig {
   static constexpr int kSoftmaxWarps = R / 4;                  // a warpgroup for every 16 rows
   static constexpr int kThreads = 32 * (kSoftmaxWarps + 2);
   static constexpr int kN = 2 * R;                             // columns of S^T
-  static constexpr int kNP = 4 * R;                            // columns of O^T
+  static constexpr int kNP = 3 * R;                            // columns of O^T
   static constexpr int kWgs = R / 16;
   static constexpr int kSlots = R <= 16 ? 5 : 4;               // ring of 16 KB tiles
-  static constexpr uint32_t kTmem = 8 * R;                     // columns: 2 S^T buffers + O^T
-  static constexpr uint32_t kPBytes = kBN * kNP;               // the terms of one tile's weights
-  // P rows (one per key) are kNP bytes: 64- or 128-byte swizzle
-  static constexpr uint64_t kPLayout = kNP == 64 ? 4 : 2;
+  static constexpr uint32_t kTmem = 8 * R;                     // columns: 2 S^T buffers + O^T (7 R), a power of two
+  // The terms of one tile's weights: 16 columns after 16 columns, each 128 keys x
+  // 16 bytes (the MMA's unswizzled layout with the columns contiguous; eight
+  // neighbouring keys are 128 bytes, which a store writes without a conflict)
+  static constexpr uint32_t kPBytes = kBN * kNP;
+  static constexpr uint32_t kPCols = kBN * 16;                 // bytes of 16 columns
 };
 
 // A piece of a sequence, as the copy warp hands it to the others.
@@ -102,7 +108,7 @@ struct __align__(1024) FewSmem {
   alignas(16) float sl2[kFewPieces][R];  // score scale of each row, log2 domain (read four at a time)
   int near[kFewPieces][R];          // the row sees the keys at least this far from the sequence's end
   // per softmax warp, for its warpgroup's 16 rows (every warp keeps its own copy):
-  alignas(16) float off[C::kSoftmaxWarps][16];  // 7 - m (read four at a time)
+  alignas(16) float off[C::kSoftmaxWarps][16];  // 6 - m (read four at a time)
   float alpha[C::kSoftmaxWarps][16];  // factor of a moved reference; v_scale / l at the end
   float top[C::kSoftmaxWarps][16];    // maxima over the warp's keys
   float sum[C::kSoftmaxWarps][16];    // row sums over the warp's keys
@@ -190,6 +196,22 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Takes the term t_i off two f16 numbers: their top bytes after rounding to them
+// (half a step of the byte; the carry runs into the exponent).  *a becomes what is
+// left, times 16.  (NaN becomes 0 or stays: the row sum has it.)
+__device__ __forceinline__ uint32_t take_term(uint32_t& a) {
+  constexpr uint32_t kSixteen = 0x4c004c00u;
+  const uint32_t t = a + 0x00800080u;
+  a = hmul2(hsub2(a, t & 0xff00ff00u), kSixteen);
+  return t;
 }
 
 // The sixteen values of every lane reduced over the warp: lane L returns the
@@ -479,7 +501,7 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)  // 32 keys at a time
                 umma_ss_f8(tmem + 2 * C::kN, make_sdesc_sw128(vbase + kk * 32 * 128, 16, 1024),
-                           make_sdesc(pbase + kk * 32 * C::kNP, 16, 8 * C::kNP, C::kPLayout), idesc_pv,
+                           make_sdesc(pbase + kk * 32 * 16, 8 * 16, C::kPCols, 0), idesc_pv,
                            (tp > t0 || kk > 0) ? 1u : 0u);
               umma_commit(&sm.p_free);
               umma_commit(&sm.empty[s]);
@@ -574,7 +596,7 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
         const bool dead = left <= 0 || ((sm.bad[jt % kFewBad] >> (k >> 4)) & 1u);
         const bool masked = __any_sync(0xffffffffu, dead || left < all_see);
         float2 w[8];        // scores, exponents, weights
-        uint32_t pt[4][4];  // the weights' e5m2 terms, four rows to a word
+        uint32_t pt[3][4];  // the weights' e5m2 terms, four rows to a word
         auto weights = [&]() {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -587,13 +609,11 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
               l[2 * i + 1] = __fadd2_rn(l[2 * i + 1], p1);
             }
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              pt[t][i] = prmt(a, c, 0x7531);  // the four top bytes
-              if (t < 3) {
-                a = hsub2(a, a & 0xff00ff00u);
-                c = hsub2(c, c & 0xff00ff00u);
-              }
+            for (int t = 0; t < 2; ++t) {
+              const uint32_t ta = take_term(a), tc = take_term(c);
+              pt[t][i] = prmt(ta, tc, 0x7531);  // the four top bytes
             }
+            pt[2][i] = prmt(a, c, 0x7531);  // what is left fits
           }
         };
         // The first tile sets the references; a later one is done again in the
@@ -636,7 +656,7 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
               if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free, (jt - 1) & 1, abort_flag));
               tc_fence_after();
 #pragma unroll
-              for (int t = 0; t < 4; ++t) {
+              for (int t = 0; t < 3; ++t) {
                 uint32_t u[16];
                 tmem_ld16_sync(tO + t * R, u);
 #pragma unroll
@@ -685,11 +705,9 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
         if (ok && jt >= 1) ok = __all_sync(0xffffffffu, mbar_wait(&sm.p_free, (jt - 1) & 1, abort_flag));
         if (ok && j == 0 && piece > 0)
           ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_free, (piece - 1) & 1, abort_flag));
-        const int sw = C::kNP == 64 ? (k >> 1) & 3 : k & 7;
-        uint8_t* prow = sm.p + k * C::kNP;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-          *reinterpret_cast<uint4*>(prow + (((t * (R / 16) + h0 / 16) ^ sw) << 4)) =
+        for (int t = 0; t < 3; ++t)
+          *reinterpret_cast<uint4*>(sm.p + (t * C::kWgs + wg) * C::kPCols + k * 16) =
               make_uint4(pt[t][0], pt[t][1], pt[t][2], pt[t][3]);
         if (wg == 0 && __any_sync(0xffffffffu, dead)) {
           // no weight falls on this key, but its V row may hold anything (NaN codes): cleared before the MMA reads it
@@ -732,15 +750,15 @@ __global__ void __launch_bounds__(FewConfig<R>::kThreads, FewConfig<R>::kCtas)
       __syncwarp();
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&sm.o_full, piece & 1, abort_flag));
       tc_fence_after();
-      float sum[16];  // the four terms' products
+      float sum[16];  // the three terms' products
       {
         uint32_t u[16], v[16];
         tmem_ld16x2_sync(tO, u, tO + R, v);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sum[e] = __uint_as_float(u[e]) + __uint_as_float(v[e]);
-        tmem_ld16x2_sync(tO + 2 * R, u, tO + 3 * R, v);
+        for (int e = 0; e < 16; ++e) sum[e] = fmaf(__uint_as_float(v[e]), 0x1p-4f, __uint_as_float(u[e]));
+        tmem_ld16_sync(tO + 2 * R, u);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sum[e] = (sum[e] + (__uint_as_float(u[e]) + __uint_as_float(v[e]))) * alpha[e];
+        for (int e = 0; e < 16; ++e) sum[e] = fmaf(__uint_as_float(u[e]), 0x1p-8f, sum[e]) * alpha[e];
       }
       if (!whole) {
         float* dst = f.part_o + (static_cast<size_t>(slot) * R + h0) * kD + k;
