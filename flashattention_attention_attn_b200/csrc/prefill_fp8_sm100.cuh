@@ -21,8 +21,12 @@
 // the row's score scale.  Two 8-bit MMAs take the time of one 16-bit MMA and
 // nothing converts K.
 //
-// Values.  P stays f16 (11 bits; P <= 2^8), so V is needed in f16, which
-// holds every e4m3 value: two warps convert V tiles from the copy ring into
+// Values.  P stays f16 (11 bits), P = 2^(x - m + 7) with m within 8 of the
+// running maximum: at most 2^15, and weights have their 11 bits down to 2^-21 of
+// the row's largest and an error of at most 2^-32 of it below, so that a long
+// row can hold most of its sum in those (with 2^(x - m), 131072 weights of 2^-21.6
+// of the largest lost 4% of their share).  So V is needed in f16, which holds
+// every e4m3 value: two warps convert V tiles from the copy ring into
 // the f16 ring, where the MMA reads them; rows past the sequence end
 // or in blocks outside the pool become zeros there.  v_scale is applied at the
 // end.
@@ -78,6 +82,7 @@ constexpr int kWarpMma = 9;
 constexpr int kWarpConv = 10;  // first of the converting warps
 constexpr int kConvWarps = 2;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr float kWeightShift = 7.0f;  // P = 2^(x - m + 7)
 constexpr uint32_t kTmemCols = 512;
 constexpr int kKStages = 3;    // K ring (e4m3, 16 KB a tile)
 constexpr int kVRaw = 2;       // V copy ring (e4m3, 16 KB a tile)
@@ -850,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         left = (!row_real ? 0 : p.causal ? min(pc.S, tok + (pc.S - pc.T) + 1) : pc.S) - pc.j0 * kBN;
       }
       float m_used = -INFINITY;  // reference max, log2 domain
-      float l = 0.f;             // running row sum relative to m_used
+      float l = 0.f;             // running sum of the row's P
       for (int j = 0; j < nt && ok; ++j) {
         ok = __all_sync(0xffffffffu, mbar_wait(&sm.s_full[t], (sn + j) & 1, abort_flag));
         if (!ok) break;
@@ -901,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float mref = (m_used == -INFINITY) ? 0.f : m_used;
         const float2 c2 = make_float2(sl2, sl2);
-        const float2 nm2 = make_float2(-mref, -mref);
+        const float2 nm2 = make_float2(kWeightShift - mref, kWeightShift - mref);
         float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
                           make_float2(0.f, 0.f)};
 #pragma unroll
@@ -944,7 +949,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i < 0) continue;
       // l = 0: no key seen, o = 0 and lse = -inf; a NaN sum stays NaN.
       const float inv_l = (my_l == 0.f) ? 0.f : p.v_scale / my_l;
-      const float lse = (my_l == 0.f) ? -INFINITY : (my_m + log2f(my_l)) * 0.69314718055994531f;
+      const float lse = (my_l == 0.f) ? -INFINITY : (my_m - kWeightShift + log2f(my_l)) * 0.69314718055994531f;
       const bool whole = pc.whole != 0;
       const int T = pc.T, qoff = pc.qoff, tok_t = pc.tok0 + t * p.tok_tile, head0 = pc.hk * p.G;
       const int r = thread_index() & 127;

@@ -569,7 +569,9 @@ int rope_axes_paged_append_fp8(const void* q, const void* k, const void* v, cons
  *   Rounding: q enters the score products as the sum of two e4m3 terms after
  *   a power-of-two scaling of its row, which is exact for elements down to
  *   2^-9 of the row's largest (2^-18 of the largest below); the weights are
- *   rounded to f16 before they meet V; sums are fp32.  Cached values that a
+ *   rounded to f16 before they meet V, scaled so that they have its 11 bits
+ *   down to 2^-20 of the row's largest weight and an error of at most 2^-31 of
+ *   it below; sums are fp32.  Cached values that a
  *   sequence holds are assumed finite; slots past its end may hold anything.
  *   Workspace, from the library's stream-ordered pool (a graph memory node
  *   in a stream capture): with num_splits <= 0 at most 40 MB, the partial

@@ -62,3 +62,13 @@ def test_few_rows_keep_small_weights(S, gap, spread, T):
         o, lse, st = run(*a[:3], False, a[3], splits=splits)
         assert st == 0
         check_sink(*a, o, lse)
+
+
+@pytest.mark.parametrize("S,gap", [(131072, 17.3), (32768, 20.2), (131072, 20.2), (131072, 21.6)])
+@pytest.mark.parametrize("spread", [False, True])
+def test_many_rows_keep_small_weights(S, gap, spread):
+    a = sink_case(S, gap, 40, spread)
+    for splits in (1, 0):
+        o, lse, st = run(*a[:3], False, a[3], splits=splits)
+        assert st == 0
+        check_sink(*a, o, lse)
