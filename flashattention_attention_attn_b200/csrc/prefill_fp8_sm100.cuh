@@ -155,6 +155,14 @@ struct Cut {
   int hk, qoff, tok0, T;
 };
 
+// Whether the merge may follow the Cut of stretch c1: its pieces' slots and its
+// head exist (rows are compared with total_q one by one).  Not so for a stretch
+// that ends no cut unit, nor where a wait gave up before the Cut was written and
+// the workspace holds what was there before.
+__host__ __device__ inline bool cut_ends_here(const Cut& c, int c1, int Hkv) {
+  return c.c0 >= 0 && c.c0 < c1 && c.hk >= 0 && c.hk < Hkv;
+}
+
 struct Params {
   __nv_bfloat16* o;            // [total_q, Hq, 128]
   float* lse;                  // [Hq, total_q] or null
@@ -486,6 +494,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int part0 = 0, part1 = 0;  // pieces that query tile 0 / 1 has taken part in
       const int il = lane & 7;
       const uint64_t kv_pol = l2_policy_evict_last();
+      // A CTA that was called off (-1: none) writes no Cut of its own.
+      auto no_cut_of = [&](int called_off) {
+        const int slot = called_off >= 0 && called_off < sm.count ? sm.count - 1 - called_off : called_off;
+        if (slot >= 0 && slot < p.num_cuts) p.cuts[slot].c0 = -1;
+      };
       bool ok = true;
       for (int i = 0; ok; ++i) {
         if (i > 0 && takes_units) {
@@ -501,8 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           asked = i;
           if (!ok) break;
           const int unit = other < 0 || other >= sm.count ? -1 : sm.count - 1 - other;
-          const int slot = unit < 0 ? other : unit;
-          if (lane == 0 && slot >= 0 && slot < p.num_cuts) p.cuts[slot].c0 = -1;
+          if (lane == 0) no_cut_of(other);
           b = p.B;
           if (unit >= 0) {
             const uint32_t w = __ballot_sync(0xffffffffu, lane < kThreads / 32 && sm.run_end[min(lane, kThreads / 32 - 1) * 32 + 31] > unit);
@@ -637,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // let the copies already issued land before shared memory is released
         if (part0 > 0) mbar_wait_drain(&sm.q_full[0], (part0 - 1) & 1);
         if (part1 > 0) mbar_wait_drain(&sm.q_full[1], (part1 - 1) & 1);
-        if (asked > 0) mbar_wait_drain(&sm.next_full, (asked - 1) & 1);
+        if (asked > 0 && mbar_wait_drain(&sm.next_full, (asked - 1) & 1)) no_cut_of(answered_cta(sm));
         for (int j = max(0, jt - kKStages); j < jt; ++j) mbar_wait_drain(&sm.k_full[j % kKStages], (j / kKStages) & 1);
         for (int j = max(0, jt - kVRaw); j < jt; ++j) mbar_wait_drain(&sm.vr_full[j % kVRaw], (j / kVRaw) & 1);
       }
@@ -1053,7 +1065,7 @@ __global__ void __launch_bounds__(256) prefill_fp8_merge(const __grid_constant__
   grid_launch_dependents();
   const int c1 = blockIdx.x;
   const Cut cut = p.cuts[c1];
-  if (cut.c0 < 0) return;
+  if (!cut_ends_here(cut, c1, p.Hkv)) return;
   const int pieces = c1 - cut.c0 + 1;
   for (int e = 0; e < kMergeRows / 8; ++e) {
     const int rr = blockIdx.y * kMergeRows + e * 8 + warp;  // row of the unit
