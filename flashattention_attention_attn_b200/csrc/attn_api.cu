@@ -1058,6 +1058,28 @@ int workspace(void** ws, size_t bytes, cudaStream_t stream, const DeviceState* s
   return ATTN_OK;
 }
 
+// Sequences with few query rows (rows = new tokens x heads of a kv head) take
+// the kernel with the rows on the MMA's columns: 16 or 32 of them, or 0 for
+// the other kernel.
+int few_rows(int max_q, int total_q, int G) {
+  const long long rows = static_cast<long long>(max_q < total_q ? max_q : total_q) * G;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 0;
+}
+
+// Length of the few-row kernel's line of key tiles at most, which it counts in
+// an int: the sequences' tiles, in num_splits > 0 ranges as long as the longest,
+// and what each sequence costs beyond them.
+long long few_line(int B, int max_tiles, int num_splits) {
+  long long tiles = max_tiles;
+  if (num_splits > 0) {
+    const int asked = num_splits < max_tiles ? num_splits : max_tiles;
+    const int chunk = (max_tiles + asked - 1) / asked;
+    tiles = static_cast<long long>((max_tiles + chunk - 1) / chunk) * chunk;
+  }
+  return B * (tiles + prefill8::kFewPieceCost);
+}
+constexpr long long kMaxFewLine = 0x7ff00000;
+
 // Few query rows per sequence.  num_splits <= 0: the tiles of all sequences
 // are dealt out evenly to one wave of CTAs.  Otherwise every sequence counts as
 // max_tiles long and each group of CTAs takes one of its num_splits ranges.
@@ -1083,8 +1105,7 @@ int launch_prefill_fp8_few(const CUtensorMap& mk, const CUtensorMap& mv, const v
   }
   f.groups = static_cast<int>(groups < 0x3fffffff ? groups : 0x3fffffff);
   const long long grid = groups * p.Hkv;
-  const long long line = static_cast<long long>(p.B) * ((f.seq_tiles ? f.seq_tiles : max_tiles) + prefill8::kFewPieceCost);
-  if (grid > 0x3fffffffLL || units > 0x7fffffffLL || line > 0x7ff00000LL) return ATTN_ERR_UNSUPPORTED;
+  if (grid > 0x3fffffffLL || units > 0x7fffffffLL) return ATTN_ERR_UNSUPPORTED;
   const size_t slots = static_cast<size_t>(grid) * 2;
   void* ws = nullptr;
   if (int rc = workspace(&ws, slots * R * (prefill8::kD + 1) * sizeof(float) + p.B * sizeof(int4), stream, st))
@@ -1113,10 +1134,7 @@ int launch_prefill_fp8(const void* q, const void* kc, const void* vc, const int3
   prefill8::Params p;
   std::memset(&p, 0, sizeof(p));
   if (max_q > total_q) max_q = total_q;
-  // Sequences with few query rows (rows = new tokens x heads of a kv head)
-  // take the kernel with the rows on the MMA's columns.
-  const long long max_rows = static_cast<long long>(max_q) * G;
-  const int few = max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : 0;
+  const int few = few_rows(max_q, total_q, G);
   p.tok_tile = (few ? few : prefill8::kBM) / G;
   CUtensorMap mq, mk, mv;
   std::memset(&mq, 0, sizeof(mq));
@@ -1152,13 +1170,12 @@ int launch_prefill_fp8(const void* q, const void* kc, const void* vc, const int3
   const long long bound = (static_cast<long long>(total_q) + static_cast<long long>(B) * (rows_cta - 1)) / rows_cta;
   if (bound < units) units = bound;
   units *= Hkv;
-  if (max_tiles > (0x7fffffff / prefill8::kBN) / 2) return ATTN_ERR_UNSUPPORTED;  // unit_keys is an int
   // Short tables have only short units, which are never cut.
   if (num_splits <= 0 && max_tiles <= prefill8::kMinCutTiles) num_splits = 1;
   const int splits_asked = num_splits > 0 ? num_splits : 1;
   const int chunk = (max_tiles + splits_asked - 1) / splits_asked;
   const int splits = (max_tiles + chunk - 1) / chunk;
-  p.unit_keys = splits * chunk * prefill8::kBN;
+  p.unit_keys = static_cast<long long>(splits) * chunk * prefill8::kBN;
   p.sms = st->sms;
   long long grid = units * splits;
   if (num_splits > 0) {  // every unit counts as num_splits ranges of equal length, a CTA takes one
@@ -1207,6 +1224,8 @@ int prefill_fp8_entry(const void* q, const void* k_cache, const void* v_cache, c
   if (d != prefill8::kD || Hq / Hkv > prefill8::kBM) return ATTN_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return ATTN_ERR_UNSUPPORTED;
   if (!aligned4(lse) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(cu_seqlens_q))
+    return ATTN_ERR_UNSUPPORTED;
+  if (few_rows(max_seqlen_q, total_q, Hq / Hkv) && few_line(B, (max_blocks + 7) / 8, num_splits) > kMaxFewLine)
     return ATTN_ERR_UNSUPPORTED;
   DeviceState* st = nullptr;
   rc = current_device_state(&st);

@@ -144,7 +144,7 @@ __device__ __forceinline__ FewSeq few_seq(const Params& p, int b) {
   q.T = __ldg(p.cu_q + b + 1) - q.qoff;
   q.S = min(max(__ldg(p.seq_lens + b), 0), p.max_blocks * 16);
   if (q.T <= 0 || q.T > p.tok_tile) q.T = 0;
-  q.tiles = q.T > 0 ? (q.S + kBN - 1) / kBN : 0;
+  q.tiles = q.T > 0 ? q.S / kBN + (q.S % kBN != 0 ? 1 : 0) : 0;  // S may be near 2^31
   return q;
 }
 

@@ -139,7 +139,7 @@ struct __align__(1024) Smem {
   int run_end[kThreads];          // units up to the end of each thread's run of sequences
   int count;                      // stretches
   int index;                      // its place among the stretches
-  int unit_keys;                  // length of every unit on the line; 0: its keys and kUnitCost
+  long long unit_keys;            // length of every unit on the line; 0: its keys and kUnitCost
   int b0, mb0;                    // the sequence and query block that it begins in
   long long rest;                 // where in them (kv heads one behind the other)
   uint32_t tmem_base;
@@ -182,7 +182,7 @@ struct Params {
   // keys of a stretch, with every unit unit_keys long; 0: the kernel decides
   // between whole units (unit_keys each) and num_cuts equal stretches
   long long stretch;
-  int unit_keys;
+  long long unit_keys;
   int sms;
   float scale_log2;            // scale * k_scale * log2(e)
   float v_scale;
@@ -253,7 +253,7 @@ struct Line {
   int qoff, T, S, nb, step;
   long long fixed;
 
-  __device__ __forceinline__ Line(const Params& p, int unit_keys, int b) {
+  __device__ __forceinline__ Line(const Params& p, long long unit_keys, int b) {
     qoff = __ldg(p.cu_q + b);
     T = max(__ldg(p.cu_q + b + 1) - qoff, 0);
     S = min(max(__ldg(p.seq_lens + b), 0), p.max_blocks * 16);
@@ -263,7 +263,7 @@ struct Line {
     fixed = unit_keys;
     if (unit_keys == 0) {
       step = p.causal ? rows : 0;
-      fixed = kUnitCost + (p.causal ? max(S - T, 0) : S);
+      fixed = static_cast<long long>(p.causal ? max(S - T, 0) : S) + kUnitCost;
     }
   }
   __device__ __forceinline__ long long unit(int mb) const {
@@ -332,7 +332,7 @@ __device__ __noinline__ void find_stretch(const Params& p, Smem& sm) {
     all_units += y;
   }
   long long stretch = p.stretch;
-  int unit_keys = p.unit_keys;
+  long long unit_keys = p.unit_keys;
   if (stretch == 0) {
     stretch = unit_keys;
     if (cut_units(all_keys, all_units, p.sms)) {
@@ -479,7 +479,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int b = sm.b0, mb = sm.mb0, hk = 0;
       // The unit's first places hold no key: an end of a stretch among them
       // counts as the unit's beginning, so that no piece is without a key.
-      const int unit_keys = sm.unit_keys, index = sm.index;
+      const long long unit_keys = sm.unit_keys;
+      const int index = sm.index;
       const bool takes_units = unit_keys > 0 && sm.stretch == unit_keys;
       int asked = 0;  // requests for another unit
       const int cost = unit_keys > 0 ? 0 : kUnitCost;
@@ -547,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const long long u = line.unit(mb);
           const long long hi = min(u, lo + (end - pos));
           const int t0 = static_cast<int>((max(lo - cost, 0LL) + kBN - 1) / kBN);
-          const int t1 = static_cast<int>(min((max(hi - cost, 0LL) + kBN - 1) / kBN, 0x7fffffffLL / kBN));
+          const int t1 = static_cast<int>(min((max(hi - cost, 0LL) + kBN - 1) / kBN, 0x7fffffffLL));
           pc.tok0 = mb * 2 * p.tok_tile;
           pc.n[0] = max(min(key_tiles(pc.tok0, p.tok_tile, line.T, line.S, p.causal), t1) - t0, 0);
           pc.n[1] = max(min(key_tiles(pc.tok0 + p.tok_tile, p.tok_tile, line.T, line.S, p.causal), t1) - t0, 0);

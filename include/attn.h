@@ -582,8 +582,10 @@ int rope_axes_paged_append_fp8(const void* q, const void* k, const void* v, cons
  *   16-byte aligned q, caches and o; sm_100.  Errors: as paged_attn_prefill;
  *   ATTN_ERR_INVALID_ARG also for a k_scale or v_scale that is not finite and
  *   positive, or a product of scale and k_scale that is not finite;
- *   ATTN_ERR_UNSUPPORTED also where B * (max_blocks / 8 + 3) tiles or the
- *   CTAs (num_splits > 0: ranges times query blocks) pass 2^30.
+ *   ATTN_ERR_UNSUPPORTED also where, with max_seqlen_q * Hq / Hkv <= 32, the
+ *   B * (max_blocks / 8 + 3) tiles pass 2^31 - 2^20 (max_blocks rounded up to
+ *   whole tiles, and with num_splits > 0 to ranges of one length), or the CTAs
+ *   (num_splits > 0: ranges times query blocks) pass 2^30.
  */
 int paged_attn_prefill_fp8(const void* q, const void* k_cache, const void* v_cache,
                            const int32_t* block_table, const int32_t* seq_lens, const int32_t* cu_seqlens_q,

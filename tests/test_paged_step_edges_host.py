@@ -1,0 +1,26 @@
+"""The serving step's limits and refusals at their borders, without a GPU."""
+
+import pytest
+import torch
+
+from tests.test_paged_step_host import UNSUPPORTED, _chunk, _without_device, lib  # noqa: F401 (lib is a fixture)
+
+WIDE = (1 << 27) - 1  # the widest table: 2^24 tiles of 128 keys
+
+
+@pytest.mark.parametrize("kw,refused", [
+    (dict(B=127, maxb=WIDE, max_q=4), False),                 # few rows: 127 (2^24 + 3) < 2^31 - 2^20
+    (dict(B=128, maxb=WIDE, max_q=4), True),
+    (dict(B=128, maxb=WIDE, max_q=8, splits=1), True),
+    (dict(B=127, maxb=WIDE, max_q=8, splits=1 << 23), False),
+    (dict(B=100, maxb=(1 << 27) - 8, max_q=8, splits=(1 << 23) + 5), False),  # ranges of two tiles: as long as the row
+    (dict(B=128, maxb=WIDE - 8, max_q=8, splits=(1 << 24) - 2), True),
+    (dict(B=128, maxb=WIDE, max_q=9), False),                 # many rows
+    (dict(B=1, maxb=WIDE, max_q=40), False),
+    (dict(B=128, maxb=WIDE, max_q=40, total_q=8), True),      # no more rows than total_q: few
+])
+def test_chunk_attention_takes_wide_tables_up_to_the_stated_limit(lib, kw, refused):  # noqa: F811
+    if not refused and torch.cuda.is_available():
+        pytest.skip("the addresses of an accepted call are made up")
+    rc = _chunk(lib, **kw)
+    assert rc == UNSUPPORTED if refused else _without_device(rc)
