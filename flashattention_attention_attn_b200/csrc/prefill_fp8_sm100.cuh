@@ -195,7 +195,8 @@ __device__ __forceinline__ float2 f16x2_to_float2(uint32_t x) {
 
 // Power-of-two scale of a query row whose largest magnitude has the bf16 bits
 // `top`: up brings it into [128, 256), down = 1 / up.  A row with NaN or
-// infinity gets down = NaN, and with it NaN scores.
+// infinity gets up = NaN, so that all its codes and with them all its scores are
+// NaN; its factor stays a number, for a masked score must stay -inf.
 struct RowScale {
   float up, down;
 };
@@ -203,8 +204,8 @@ struct RowScale {
 __device__ __forceinline__ RowScale row_scale(uint32_t top) {
   const int ex = max(static_cast<int>(top >> 7) - 127, -110);  // keeps 2^(7 - ex) finite
   RowScale s;
-  s.up = __int_as_float((7 - ex + 127) << 23);
-  s.down = ex == 128 ? __int_as_float(0x7fffffff) : __int_as_float((ex - 7 + 127) << 23);
+  s.up = ex == 128 ? __int_as_float(0x7fffffff) : __int_as_float((7 - ex + 127) << 23);
+  s.down = __int_as_float((ex - 7 + 127) << 23);
   return s;
 }
 
@@ -212,7 +213,7 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top) {
 // would be NaN.
 __device__ __forceinline__ float row_score_scale(float scale_log2, const RowScale& rs) {
   const float s = scale_log2 * rs.down;
-  return s < 1.2e-38f ? 1.2e-38f : s;  // false for NaN
+  return s < 1.2e-38f ? 1.2e-38f : s;
 }
 
 // 16 bf16 elements, scaled, as e4m3 terms: hi = e4m3(x), lo = e4m3(x - hi).
