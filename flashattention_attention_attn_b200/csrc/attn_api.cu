@@ -1322,6 +1322,8 @@ int rope_append_entry(int mode, const void* q, const void* k, const void* v, con
     return ATTN_ERR_INVALID_ARG;
   p.inv_k_scale = 1.f / k_scale;
   p.inv_v_scale = 1.f / v_scale;
+  // (at 2^-128 and below the reciprocal overflows: zeros would become NaN codes)
+  if (!std::isfinite(p.inv_k_scale) || !std::isfinite(p.inv_v_scale)) return ATTN_ERR_INVALID_ARG;
   p.k_cache = k_cache;
   p.v_cache = v_cache;
   return rope_entry(mode, p, freq_axis, rot_dim, num_axes, stream);

@@ -543,7 +543,8 @@ int rope_axes_paged_append(const void* q, const void* k, const void* v, const in
  * reciprocals of the scales, round to nearest even, saturated to +-448; NaN
  * stays NaN).
  *   Supported: d == 128; otherwise as rope_axes_paged_append;
- *   ATTN_ERR_INVALID_ARG also for a scale that is not finite and positive.
+ *   ATTN_ERR_INVALID_ARG also for a scale that is not finite and positive or
+ *   whose fp32 reciprocal is not finite (2^-128 and below).
  */
 int rope_axes_paged_append_fp8(const void* q, const void* k, const void* v, const int32_t* positions,
                                const float* inv_freq, const uint8_t* freq_axis, const int32_t* slot_map,

@@ -3,7 +3,7 @@
 import pytest
 import torch
 
-from tests.test_paged_step_host import UNSUPPORTED, _chunk, _without_device, lib  # noqa: F401 (lib is a fixture)
+from tests.test_paged_step_host import INVALID, UNSUPPORTED, _append, _chunk, _without_device, lib  # noqa: F401 (lib is a fixture)
 
 WIDE = (1 << 27) - 1  # the widest table: 2^24 tiles of 128 keys
 
@@ -24,3 +24,17 @@ def test_chunk_attention_takes_wide_tables_up_to_the_stated_limit(lib, kw, refus
         pytest.skip("the addresses of an accepted call are made up")
     rc = _chunk(lib, **kw)
     assert rc == UNSUPPORTED if refused else _without_device(rc)
+
+
+@pytest.mark.parametrize("scales,refused", [
+    ((2.0 ** -130, 1.0), True),      # the reciprocal is infinite in fp32: zeros would become NaN codes
+    ((1.0, 2.0 ** -149), True),
+    ((2.0 ** -128, 1.0), True),
+    ((2.0 ** -127, 2.0 ** -126), False),
+    ((3e38, 1.0), False),
+])
+def test_append_fp8_refuses_scales_without_a_reciprocal(lib, scales, refused):  # noqa: F811
+    if not refused and torch.cuda.is_available():
+        pytest.skip("the addresses of an accepted call are made up")
+    rc = _append(lib, fp8=True, scales=scales)
+    assert rc == INVALID if refused else _without_device(rc)
