@@ -36,9 +36,10 @@ Plan: block_table [B,max_blocks] is updated in place, the other outputs are
 new; pos_offsets may be None.  Rotary: q [n,Hq,d], k [n,Hkv,d] (rows of heads
 may lie further apart, as columns of a fused projection do), positions
 [axes,n] int32, inv_freq [rot/2] fp32, freq_axis a list of rot/2 axes (empty:
-axis 0); the caches are written in place.  rope_axes' gradient is captured into a
-graph under the rule of every torch operator: no eager graph of the same
-leaves may live on the default stream meanwhile.
+axis 0); the caches are written in place.  rope_axes has a gradient for q and
+k, to the first order (rope_axes_bwd has none); an inv_freq that requires one is
+refused.  It is captured into a graph under the rule of every torch operator: no
+eager graph of the same leaves may live on the default stream meanwhile.
 """
 
 from __future__ import annotations
@@ -277,6 +278,8 @@ rope_axes_bwd.register_fake(_rope_fake)
 
 def _rope_setup(ctx, inputs, output):
     _, _, positions, inv_freq, ctx.freq_axis, ctx.adjacent = inputs
+    if ctx.needs_input_grad[3]:
+        raise ValueError("inv_freq requires a gradient, which rope_axes does not compute: pass inv_freq.detach()")
     ctx.save_for_backward(positions, inv_freq)
 
 

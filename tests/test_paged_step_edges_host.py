@@ -38,3 +38,21 @@ def test_append_fp8_refuses_scales_without_a_reciprocal(lib, scales, refused):  
         pytest.skip("the addresses of an accepted call are made up")
     rc = _append(lib, fp8=True, scales=scales)
     assert rc == INVALID if refused else _without_device(rc)
+
+
+def test_rope_op_refuses_frequencies_that_want_a_gradient():
+    """None is computed for them, so a call that would leave it out silently is refused; q and k alone train."""
+    import flashattention_attention_attn_b200.torch_ops  # noqa: F401
+    rope = torch.ops.fa_b200.rope_axes
+    with torch._subclasses.FakeTensorMode():
+        q, k = (torch.empty(5, h, 64, dtype=torch.bfloat16, requires_grad=True) for h in (4, 2))
+        f, pos = torch.empty(32, requires_grad=True), torch.empty(1, 5, dtype=torch.int32)
+        with pytest.raises(ValueError, match="inv_freq"):
+            rope(q, k, pos, f, [], False)
+        with pytest.raises(ValueError, match="inv_freq"):
+            rope(q.detach(), k.detach(), pos, f, [], False)
+        a, b = rope(q, k, pos, f.detach(), [], False)
+        dq, dk = torch.autograd.grad((a, b), (q, k), (torch.empty_like(a), torch.empty_like(b)))
+        assert dq.shape == q.shape and dk.shape == k.shape
+        with torch.no_grad():
+            assert rope(q, k, pos, f, [], False)[0].shape == q.shape
