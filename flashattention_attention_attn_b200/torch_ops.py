@@ -176,12 +176,18 @@ def _(o_parts, lse_parts):
     return o_parts.new_empty(o_parts.shape[1:], dtype=torch.bfloat16)
 
 
+def _packed(x: torch.Tensor) -> torch.Tensor:
+    """x without gaps and on a 16-byte boundary, copied only if it is not (a slice of a flat buffer may be packed and
+    lie off the boundary, where contiguous() copies nothing)."""
+    return x.contiguous() if not x.is_contiguous() or x.data_ptr() % 16 == 0 else x.clone()
+
+
 def _rows(x: torch.Tensor) -> torch.Tensor:
     """x [n, H, d] with the heads of a row side by side and the rows apart, copied only if they are not
     (a gradient that was expanded over the tokens has rows that share their memory)."""
     if (x.stride(-1) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]) or x.stride(0) % 8 or x.data_ptr() % 16
             or (x.shape[0] > 1 and x.stride(0) < x.shape[1] * x.shape[2])):
-        return x.contiguous()
+        return _packed(x)
     return x
 
 
@@ -349,7 +355,7 @@ def paged_attn_prefill_fp8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     _need(True, _INT32, block_table=block_table, seq_lens=seq_lens, cu_seqlens_q=cu_seqlens_q)
     _shape(q=(q, (None, None, None)), k_cache=(k_cache, (None, None, None, None)),
            cu_seqlens_q=(cu_seqlens_q, (None,)))
-    q = q.contiguous()
+    q = _packed(q)
     total_q, Hq, d = q.shape
     num_blocks, block_size, Hkv = k_cache.shape[:3]
     B = cu_seqlens_q.shape[0] - 1
