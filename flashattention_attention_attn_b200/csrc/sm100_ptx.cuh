@@ -352,7 +352,7 @@ __host__ __device__ constexpr uint32_t make_sdesc_hi_sw128(uint32_t sbo_bytes) {
   return (sbo_bytes >> 4) | 1u << 14 | 2u << 29;
 }
 
-// The same with any swizzle: layout 2 = 128-byte, 4 = 64-byte, 6 = 32-byte.
+// The same with any swizzle: layout 0 = none, 2 = 128-byte, 4 = 64-byte, 6 = 32-byte.
 __device__ __forceinline__ uint64_t make_sdesc(uint32_t saddr, uint32_t lbo_bytes, uint32_t sbo_bytes,
                                                uint64_t layout) {
   return uint64_t((saddr >> 4) & 0x3FFFu) | uint64_t((lbo_bytes >> 4) & 0x3FFFu) << 16 |
@@ -431,13 +431,6 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Maximum over the warp (NaN only where every lane is NaN).
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
 
