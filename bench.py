@@ -65,11 +65,11 @@ DEFAULT_WORKLOAD = "long"
 # bench reports null until a new capture replaces it.
 TRAFFIC = {
     # set: {"prefill": bytes per launch, "decode": bytes per call (split + combine), "csrc": hash}
-    "long": {"prefill": 385.87e6, "decode": 539.64e6, "csrc": "9898647b944a1719"},
-    "step": {"prefill": 12.65e6, "decode": 605.03e6, "csrc": "9898647b944a1719"},
-    "fp8": {"prefill": 12.65e6, "decode": 306.21e6, "csrc": "9898647b944a1719"},
-    "varlen": {"prefill": 279.74e6, "decode": 605.02e6, "csrc": "9898647b944a1719"},
-    "chunked": {"prefill": 209.86e6, "decode": 605.07e6, "csrc": "9898647b944a1719"},
+    "long": {"prefill": 384.17e6, "decode": 539.63e6, "csrc": "f3c34d6f15b045a8"},
+    "step": {"prefill": 12.65e6, "decode": 605.07e6, "csrc": "f3c34d6f15b045a8"},
+    "fp8": {"prefill": 12.65e6, "decode": 306.14e6, "csrc": "f3c34d6f15b045a8"},
+    "varlen": {"prefill": 280.31e6, "decode": 605.14e6, "csrc": "f3c34d6f15b045a8"},
+    "chunked": {"prefill": 210.31e6, "decode": 605.06e6, "csrc": "f3c34d6f15b045a8"},
 }
 
 

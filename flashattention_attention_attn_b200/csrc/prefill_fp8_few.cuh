@@ -50,7 +50,7 @@
 // joins them.
 //
 // Measured, G = 4, 8 kv heads: 64 sequences of 4 drafted tokens over 256 to 4096
-// keys 65 us (302 MB of codes, 4.6 TB/s), 8 tokens over 131072 keys 66 us
+// keys 65 us (302 MB of codes, 4.6 TB/s), 8 tokens over 131072 keys 65 us
 // (268 MB, 4.1 TB/s), launch and merge included; with the rows on the lanes of
 // the other kernel 276 and 200 us.
 #pragma once

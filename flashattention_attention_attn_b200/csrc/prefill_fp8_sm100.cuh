@@ -54,9 +54,14 @@
 // the FMA pipe, P handed over in halves, the tiles' exponentials in strict turns.
 // Straight-line code is kept short (loops over chunks of the output, of q and of
 // V stay rolled): what runs once a piece is fetched cold.
-// Measured, G = 4, 8 kv heads: 2048 tokens at 32k 906 us (1.2 PFLOP/s of 16-bit
-// work), 8 x 512 tokens at .5k to 7.7k 217 us, 4096 tokens from nothing 150 us;
-// 33 sequences of 0 to 300 tokens at 0 to 2500, G = 6, 4 kv heads, 184 us.
+// That is 838 us of 2048 tokens at 32k.  8 x 512 tokens below: 161 us, 211 us with
+// three tiles' time for each start and the order in which units start (sequence
+// by sequence; all of them longest first would give 185).  The ragged batch: 92 us
+// and, with starts and order, 125; the rest of its time is not accounted for.
+// Measured, G = 4, 8 kv heads: 2048 tokens at 32k 900 us (1.2 PFLOP/s of 16-bit
+// work; 1030 us in a long series of calls, under the power cap), 8 x 512 tokens at
+// .5k to 7.7k 218 us (230 so), 4096 tokens from nothing 150 us;
+// 33 sequences of 0 to 300 tokens at 0 to 2500, G = 6, 4 kv heads, 179 us.
 #pragma once
 
 #include <cuda_fp16.h>

@@ -13,8 +13,11 @@
 // 2^-7 radians), reduced there to a fraction of a turn and handed to
 // sincospif in fp32.  The rotation is fp32, rounded once to the output type.
 //
-// Every byte is read once and written once, so HBM bounds the call (and the
-// launch, for a few tokens).  A work unit is 16 elements (two 16-byte accesses)
+// Every byte is read once and written once, so HBM bounds a long call (and the
+// launch, for a few tokens).  The FP8 cache write of 4096 tokens is bound by
+// latency instead: a CTA takes its units in six rounds of loads, use and stores,
+// one after the other, in less than one wave of CTAs, and reads 2.75 TB/s while its
+// writes stay in L2.  A work unit is 16 elements (two 16-byte accesses)
 // of one head: 8 pairs.  A CTA takes `tpc` tokens; its threads first set out the
 // loads of kUnroll units each, and meanwhile make the tokens' cos / sin into
 // shared memory, which all Hq + Hkv heads of a token share.  Measured (calls in
